@@ -42,7 +42,9 @@ typedef enum {
     RA_ERR_WORKSPACE = 3,       /* workspace too small or not prepared for this problem */
     RA_ERR_CUDA = 4,            /* a CUDA runtime call or launch failed */
     RA_ERR_DEVICE_TIMEOUT = 5,  /* a bounded device-side wait ran out */
-    RA_ERR_DEVICE_BOUNDS = 6    /* a device-side self-check found a bad index */
+    RA_ERR_DEVICE_BOUNDS = 6,   /* a device-side self-check found a bad index */
+    RA_ERR_CACHE_FULL = 7       /* a cache has too few free pages, or a sequence too few
+                                 * table entries; the call changed nothing */
 } ra_status;
 
 typedef enum {
@@ -273,6 +275,151 @@ ra_status ra_rotate_quantize_qkv_noalloc(const ra_problem *p, const void *q, con
  * were not the problem's: overlapping calls), RA_ERR_DEVICE_TIMEOUT,
  * RA_ERR_DEVICE_BOUNDS or RA_ERR_CUDA.  Allocates nothing. */
 ra_status ra_noalloc_check_device_error(ra_stream stream);
+
+/* ---- packed sequences --------------------------------------------------- */
+
+typedef enum { RA_FP16 = 0, RA_BF16 = 1 } ra_dtype;
+
+/* Attention over n_seqs sequences of different lengths, packed one behind the
+ * other: sequence i has query tokens [cu_q[i], cu_q[i+1]) and key tokens
+ * [cu_k[i], cu_k[i+1]); query head h reads key head h / (Hq / Hkv).
+ *   o_t = sum_j p_tj v_j / sum_j p_tj,   p_tj = exp(scale q_t . k_j),
+ * over all keys of the sequence, or, with causal != 0, over keys j <= t + Lk -
+ * Lq (t and j counted within the sequence: the last query token sees every
+ * key, so a chunk of a prompt attends to what came before it).  A token that
+ * sees no key gets zeros and a log-sum-exp of -infinity; rows behind
+ * cu_q[n_seqs] are left as they were.  Keys and values that a token does not
+ * see do not reach it, whatever they hold.
+ * There is no position encoding: queries and keys come encoded. */
+typedef struct {
+    int n_seqs;                 /* >= 1 */
+    int Hq, Hkv, d;             /* Hq a multiple of Hkv, Hq / Hkv <= 128; d == 128 */
+    int dtype;                  /* ra_dtype of q, k, v and o */
+    int causal;                 /* 0 or 1 */
+    int total_q, total_k;       /* rows of q and o, and of k and v: at least cu_q[n_seqs], cu_k[n_seqs] */
+    double scale;               /* > 0, or 0 for 1 / sqrt(d) */
+    long long q_token, q_head;  /* strides in elements: multiples of 8, at least d; an */
+    long long k_token, k_head;  /* element of the head dimension follows the last. */
+    long long v_token, v_head;
+    long long o_token, o_head;  /* o's rows must not overlap */
+} ra_packed;
+
+/* Bytes of the call's workspace (0 if the problem is invalid): a header, and
+ * the partial rows of a call that splits its keys over the GPU (few rows over
+ * many keys).  The first 256 bytes must be zero before the first use (they
+ * hold the error word of ra_check_device_error). */
+size_t ra_packed_workspace_bytes(const ra_packed *p);
+
+/* q, o: total_q rows; k, v: total_k rows; cu_q, cu_k: device int32 [n_seqs +
+ * 1], ascending from 0; lse: device float [total_q][Hq], the natural
+ * logarithm of each row's sum, or NULL.  The lengths are read on the device
+ * alone: a captured call replays with the lengths of its moment.  Offsets
+ * that descend or leave the buffers are reported (RA_ERR_DEVICE_BOUNDS) and
+ * that sequence is left out. */
+ra_status ra_packed_attention_fwd(const ra_packed *p, const void *q, const void *k, const void *v, const int *cu_q,
+                                  const int *cu_k, void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                  ra_stream stream);
+
+/* ---- paged cache ---------------------------------------------------------- */
+
+/* Keys and values of up to max_seqs sequences in pages of page_size tokens,
+ * shared by `layers` layers: page p of layer l holds, for every key head,
+ * page_size consecutive tokens. */
+typedef struct {
+    int layers;                 /* >= 1 */
+    int n_pages;                /* >= 1 */
+    int page_size;              /* 16, 32, 64 or 128 tokens */
+    int Hkv, d;                 /* d == 128 */
+    int dtype;                  /* ra_dtype */
+    int max_seqs, max_pages;    /* rows and columns of the table; max_seqs * max_pages < 2^31,
+                                 * max_pages * page_size < 2^30 */
+} ra_cache_problem;
+
+/* Device memory of a cache:
+ *   k, v  : [layers][n_pages][Hkv][page_size][128]
+ *   refs  : int32 [n_pages], how many table entries name the page (0: free)
+ *   lens  : int32 [max_seqs], tokens of the sequence in each row
+ *   table : int32 [max_seqs][max_pages], the pages of each row, -1 behind the last
+ * The state (refs, lens, table) is changed by the calls below in stream order;
+ * a program may also copy it, and put a copy back. */
+typedef struct {
+    void *k, *v;
+    int *refs, *lens, *table;
+} ra_cache;
+
+ra_status ra_cache_validate(const ra_cache_problem *p);
+size_t ra_cache_pool_bytes(const ra_cache_problem *p);    /* one buffer: k, then v (0 if invalid) */
+size_t ra_cache_state_bytes(const ra_cache_problem *p);   /* one buffer: refs, lens, table, each aligned to 256 bytes */
+ra_status ra_cache_bind(const ra_cache_problem *p, void *pool, size_t pool_bytes, void *state, size_t state_bytes,
+                        ra_cache *out);
+size_t ra_cache_workspace_bytes(const ra_cache_problem *p);   /* of extend, write, fork, free, compact; the first
+                                                               * 256 bytes zero before the first use */
+
+/* An empty cache: every page free, every row of length 0. */
+ra_status ra_cache_init(const ra_cache_problem *p, const ra_cache *c, ra_stream stream);
+
+/* In the calls below `seqs`, `parents`, `children` are device int32 lists of
+ * table rows, n <= max_seqs of them; an entry of -1 is passed over (a padded
+ * batch).  A call whose list names a row twice or outside the table, whose
+ * counts are negative (RA_ERR_DEVICE_BOUNDS) or that needs more pages than
+ * are free or a longer row than max_pages (RA_ERR_CACHE_FULL) changes nothing
+ * and is reported by ra_check_device_error. */
+
+/* Row seqs[i] grows by n_new[i] >= 0 tokens (device int32): new pages are the
+ * lowest-numbered free ones, in list order.  Their slots are unwritten. */
+ra_status ra_cache_extend(const ra_cache_problem *p, const ra_cache *c, const int *seqs, const int *n_new, int n,
+                          void *workspace, size_t workspace_bytes, ra_stream stream);
+
+/* Writes the last tokens of each row in one layer: row seqs[i] gets tokens
+ * [cu_new[i], cu_new[i+1]) of k and v (cu_new NULL: token i), at positions
+ * lens - count and on.  k, v: [total][Hkv][128] with the given strides
+ * (elements; multiples of 8).  A row is named once at most. */
+ra_status ra_cache_write(const ra_cache_problem *p, const ra_cache *c, int layer, const int *seqs, const int *cu_new,
+                         int n, int total, const void *k, const void *v, long long k_token, long long k_head,
+                         long long v_token, long long v_head, void *workspace, size_t workspace_bytes,
+                         ra_stream stream);
+
+/* Row children[i] (empty, named once, no parent of this call) becomes a copy
+ * of row parents[i]: it shares the parent's full pages; a part-filled last
+ * page is copied, its filled tokens in every layer, into a page of its own.
+ * A parent may have several children.  Two launches. */
+ra_status ra_cache_fork(const ra_cache_problem *p, const ra_cache *c, const int *parents, const int *children, int n,
+                        void *workspace, size_t workspace_bytes, ra_stream stream);
+
+/* Rows become empty; a page that no row names any more is free. */
+ra_status ra_cache_free(const ra_cache_problem *p, const ra_cache *c, const int *seqs, int n, void *workspace,
+                        size_t workspace_bytes, ra_stream stream);
+
+/* Moves pages so that the n live ones are pages 0 .. n-1: the i-th free page
+ * below n takes the i-th live page at or above n, in every layer, and the
+ * table follows.  Two launches. */
+ra_status ra_cache_compact(const ra_cache_problem *p, const ra_cache *c, void *workspace, size_t workspace_bytes,
+                           ra_stream stream);
+
+/* Attention of a batch's newest tokens over a cache's pages in one layer. */
+typedef struct {
+    int n_seqs, Hq;             /* Hq a multiple of Hkv, Hq / Hkv <= 128 */
+    int total_q;                /* rows of q and o */
+    int layer;
+    int shared;                 /* leading tokens whose pages all sequences of the call share; a
+                                 * multiple of page_size; 0: none */
+    double scale;               /* > 0, or 0 for 1 / sqrt(d) */
+    long long q_token, q_head, o_token, o_head;   /* strides, as in ra_packed */
+} ra_cache_attn;
+
+size_t ra_cache_attention_workspace_bytes(const ra_cache_problem *p, const ra_cache_attn *a);
+
+/* Sequence i is table row seqs[i] (-1: none, its rows get zeros) with query
+ * tokens [cu_q[i], cu_q[i+1]) (cu_q NULL: token i), the last ones of its
+ * lens[seqs[i]] tokens, written before the call; each sees the tokens up to
+ * itself.  Rows may be named more than once.
+ * The first `shared` tokens are read once for the whole batch, from the
+ * longest sequence's pages: every sequence must hold the same pages there
+ * (fork makes them so) as far as it reaches.  o, lse, workspace, errors: as in
+ * ra_packed_attention_fwd.  Two launches. */
+ra_status ra_cache_attention_fwd(const ra_cache_problem *p, const ra_cache *c, const ra_cache_attn *a, const void *q,
+                                 const int *seqs, const int *cu_q, void *o, float *lse, void *workspace,
+                                 size_t workspace_bytes, ra_stream stream);
 
 /* ---- test hooks ------------------------------------------------------- */
 

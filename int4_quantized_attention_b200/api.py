@@ -19,9 +19,10 @@ LIB_PATH = os.path.join(PKG, "librotate_attn_bounds.so" if os.environ.get("RA_LI
                         else "librotate_attn.so")
 
 RA_OK, RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_WORKSPACE, RA_ERR_CUDA, \
-    RA_ERR_DEVICE_TIMEOUT, RA_ERR_DEVICE_BOUNDS = range(7)
+    RA_ERR_DEVICE_TIMEOUT, RA_ERR_DEVICE_BOUNDS, RA_ERR_CACHE_FULL = range(8)
 ROT = {"none": 0, "interleaved": 1, "half": 2, "full": 3, "blocks_interleaved": 4, "blocks_half": 5}
 P_MODE = {"range": 0, "symmetric": 1}       # ra_p_mode
+DTYPE_FP16, DTYPE_BF16 = 0, 1               # ra_dtype
 
 
 class RotateAttnError(RuntimeError):
@@ -46,10 +47,39 @@ class Qkv4(ctypes.Structure):
                 ("vsum", ctypes.c_void_p)]
 
 
+class Packed(ctypes.Structure):
+    """Mirror of ra_packed."""
+    _fields_ = [(n, ctypes.c_int) for n in ("n_seqs", "Hq", "Hkv", "d", "dtype", "causal", "total_q", "total_k")] + \
+        [("scale", ctypes.c_double)] + \
+        [(n, ctypes.c_longlong) for n in ("q_token", "q_head", "k_token", "k_head", "v_token", "v_head",
+                                          "o_token", "o_head")]
+
+
+class CacheProblem(ctypes.Structure):
+    """Mirror of ra_cache_problem."""
+    _fields_ = [(n, ctypes.c_int) for n in ("layers", "n_pages", "page_size", "Hkv", "d", "dtype", "max_seqs",
+                                            "max_pages")]
+
+
+class Cache(ctypes.Structure):
+    """Mirror of ra_cache (device pointers)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "refs", "lens", "table")]
+
+
+class CacheAttn(ctypes.Structure):
+    """Mirror of ra_cache_attn."""
+    _fields_ = [(n, ctypes.c_int) for n in ("n_seqs", "Hq", "total_q", "layer", "shared")] + \
+        [("scale", ctypes.c_double)] + \
+        [(n, ctypes.c_longlong) for n in ("q_token", "q_head", "o_token", "o_head")]
+
+
 _lib = None
 _P = ctypes.POINTER(Problem)
 _V = ctypes.c_void_p
 _SZ = ctypes.c_size_t
+
+_PK, _CP, _C, _CA = (ctypes.POINTER(t) for t in (Packed, CacheProblem, Cache, CacheAttn))
+_I, _LL = ctypes.c_int, ctypes.c_longlong
 
 _SIGNATURES = {
     "ra_seq_len": (ctypes.c_int, [_P]),
@@ -78,6 +108,21 @@ _SIGNATURES = {
     "ra_debug_timeout_probe": (ctypes.c_int, [_V, _SZ, _V]),
     "ra_measure_mma_i8": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _V, _SZ, _V]),
     "ra_debug_ex2": (ctypes.c_int, [_V, _V, ctypes.c_int, _V]),
+    "ra_packed_workspace_bytes": (_SZ, [_PK]),
+    "ra_packed_attention_fwd": (_I, [_PK, _V, _V, _V, _V, _V, _V, _V, _V, _SZ, _V]),
+    "ra_cache_validate": (_I, [_CP]),
+    "ra_cache_pool_bytes": (_SZ, [_CP]),
+    "ra_cache_state_bytes": (_SZ, [_CP]),
+    "ra_cache_bind": (_I, [_CP, _V, _SZ, _V, _SZ, _C]),
+    "ra_cache_workspace_bytes": (_SZ, [_CP]),
+    "ra_cache_init": (_I, [_CP, _C, _V]),
+    "ra_cache_extend": (_I, [_CP, _C, _V, _V, _I, _V, _SZ, _V]),
+    "ra_cache_write": (_I, [_CP, _C, _I, _V, _V, _I, _I, _V, _V, _LL, _LL, _LL, _LL, _V, _SZ, _V]),
+    "ra_cache_fork": (_I, [_CP, _C, _V, _V, _I, _V, _SZ, _V]),
+    "ra_cache_free": (_I, [_CP, _C, _V, _I, _V, _SZ, _V]),
+    "ra_cache_compact": (_I, [_CP, _C, _V, _SZ, _V]),
+    "ra_cache_attention_workspace_bytes": (_SZ, [_CP, _CA]),
+    "ra_cache_attention_fwd": (_I, [_CP, _C, _CA, _V, _V, _V, _V, _V, _V, _SZ, _V]),
 }
 
 
@@ -267,7 +312,313 @@ def measure_mma_i8(n: int, iters: int, ctas: int, workspace, stream=None) -> Non
                                                         _stream(stream)))
 
 
+def packed_workspace_bytes(p: Packed) -> int:
+    return lib().ra_packed_workspace_bytes(ctypes.byref(p))
+
+
+def packed_attention_fwd(p: Packed, q, k, v, cu_q, cu_k, o, lse, workspace, stream=None) -> None:
+    _check("ra_packed_attention_fwd",
+           lib().ra_packed_attention_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(o),
+                                         _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def cache_validate(p: CacheProblem) -> int:
+    return lib().ra_cache_validate(ctypes.byref(p))
+
+
+def cache_pool_bytes(p: CacheProblem) -> int:
+    return lib().ra_cache_pool_bytes(ctypes.byref(p))
+
+
+def cache_state_bytes(p: CacheProblem) -> int:
+    return lib().ra_cache_state_bytes(ctypes.byref(p))
+
+
+def cache_bind(p: CacheProblem, pool, state) -> Cache:
+    out = Cache()
+    _check("ra_cache_bind", lib().ra_cache_bind(ctypes.byref(p), _ptr(pool), pool.numel() * pool.element_size(),
+                                                _ptr(state), state.numel() * state.element_size(), ctypes.byref(out)))
+    return out
+
+
+def cache_workspace_bytes(p: CacheProblem) -> int:
+    return lib().ra_cache_workspace_bytes(ctypes.byref(p))
+
+
+def cache_init(p: CacheProblem, c: Cache, stream=None) -> None:
+    _check("ra_cache_init", lib().ra_cache_init(ctypes.byref(p), ctypes.byref(c), _stream(stream)))
+
+
+def cache_extend(p: CacheProblem, c: Cache, seqs, n_new, workspace, stream=None) -> None:
+    _check("ra_cache_extend",
+           lib().ra_cache_extend(ctypes.byref(p), ctypes.byref(c), _ptr(seqs), _ptr(n_new), seqs.numel(),
+                                 _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def cache_write(p: CacheProblem, c: Cache, layer: int, seqs, cu_new, k, v, workspace, stream=None) -> None:
+    """k, v: [tokens, Hkv, 128]."""
+    _check("ra_cache_write",
+           lib().ra_cache_write(ctypes.byref(p), ctypes.byref(c), layer, _ptr(seqs), _ptr(cu_new), seqs.numel(),
+                                k.shape[0], _ptr(k), _ptr(v), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                                _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def cache_fork(p: CacheProblem, c: Cache, parents, children, workspace, stream=None) -> None:
+    _check("ra_cache_fork",
+           lib().ra_cache_fork(ctypes.byref(p), ctypes.byref(c), _ptr(parents), _ptr(children), children.numel(),
+                               _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def cache_free(p: CacheProblem, c: Cache, seqs, workspace, stream=None) -> None:
+    _check("ra_cache_free", lib().ra_cache_free(ctypes.byref(p), ctypes.byref(c), _ptr(seqs), seqs.numel(),
+                                                _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def cache_compact(p: CacheProblem, c: Cache, workspace, stream=None) -> None:
+    _check("ra_cache_compact", lib().ra_cache_compact(ctypes.byref(p), ctypes.byref(c), _ptr(workspace),
+                                                      workspace.numel(), _stream(stream)))
+
+
+def cache_attention_workspace_bytes(p: CacheProblem, a: CacheAttn) -> int:
+    return lib().ra_cache_attention_workspace_bytes(ctypes.byref(p), ctypes.byref(a))
+
+
+def cache_attention_fwd(p: CacheProblem, c: Cache, a: CacheAttn, q, seqs, cu_q, o, lse, workspace,
+                        stream=None) -> None:
+    _check("ra_cache_attention_fwd",
+           lib().ra_cache_attention_fwd(ctypes.byref(p), ctypes.byref(c), ctypes.byref(a), _ptr(q), _ptr(seqs),
+                                        _ptr(cu_q), _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(),
+                                        _stream(stream)))
+
+
 # ---------------------------------------------------------------- convenience
+
+def _bad(call: str, detail: str):
+    lib()
+    return RotateAttnError(call, RA_ERR_INVALID_ARG, detail)
+
+
+def _dtype(call: str, dtype) -> int:
+    import torch
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise _bad(call, f"dtype {dtype}: float16 or bfloat16")
+    return DTYPE_FP16 if dtype == torch.float16 else DTYPE_BF16
+
+
+def _rows(call: str, name: str, t, dtype, device, heads=None, tokens=None):
+    """Checks a [tokens, heads, 128] tensor whose last dimension is contiguous."""
+    if t.dim() != 3 or t.dtype != dtype or t.device != device or t.shape[2] != 128 or \
+            (t.stride(2) != 1 and t.numel()) or (heads is not None and t.shape[1] != heads) or \
+            (tokens is not None and t.shape[0] != tokens):
+        raise _bad(call, f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}; want "
+                         f"[{'tokens' if tokens is None else tokens}, {'heads' if heads is None else heads}, 128] "
+                         f"{dtype} on {device} with a contiguous last dimension")
+
+
+def _ints(call: str, name: str, t, device, n=None):
+    import torch
+    if t.dim() != 1 or t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or \
+            (n is not None and t.numel() != n):
+        raise _bad(call, f"{name}: a contiguous 1-D int32 tensor{'' if n is None else f' of {n}'} on {device}")
+
+
+class _Workspace:
+    """A workspace that grows with what it is asked for.  Buffers that were
+    outgrown are kept, since a captured graph may still use them."""
+
+    def __init__(self, device):
+        self.device, self.buffers = device, []
+
+    def get(self, need: int):
+        import torch
+        if not self.buffers or self.buffers[-1].numel() < need:
+            size = need if not self.buffers else max(need, 2 * self.buffers[-1].numel())
+            self.buffers.append(torch.zeros((size,), dtype=torch.uint8, device=self.device))
+        return self.buffers[-1]
+
+    def check(self):
+        import torch
+        with torch.cuda.device(self.device):
+            for b in self.buffers:
+                check_device_error(b)
+
+
+class PackedAttention:
+    """Attention over packed sequences of different lengths (ra_packed_attention_fwd):
+    owns, through PyTorch, the workspace of one stream of calls and runs on the
+    current stream.  Calls of one object must not overlap on the GPU."""
+
+    def __init__(self, device="cuda"):
+        import torch
+        self.device = torch.empty(0, device=device).device
+        self._ws = _Workspace(self.device)
+
+    def forward(self, q, k, v, cu_q, cu_k, causal: bool = True, scale: float = 0.0, out=None, lse=None,
+                return_lse: bool = False):
+        """q [total_q, Hq, 128], k and v [total_k, Hkv, 128], fp16 or bf16, any
+        token and head strides that are multiples of 8 elements; cu_q and cu_k
+        int32 [n + 1] on the device.  Returns out, or (out, lse)."""
+        import torch
+        call = "packed_attention"
+        dtype = q.dtype
+        code = _dtype(call, dtype)
+        _rows(call, "q", q, dtype, self.device)
+        _rows(call, "k", k, dtype, self.device)
+        _rows(call, "v", v, dtype, self.device, k.shape[1], k.shape[0])
+        _ints(call, "cu_q", cu_q, self.device)
+        _ints(call, "cu_k", cu_k, self.device, cu_q.numel())
+        total_q, Hq = q.shape[0], q.shape[1]
+        if out is None:
+            out = torch.empty((total_q, Hq, 128), dtype=dtype, device=self.device)
+        else:
+            _rows(call, "out", out, dtype, self.device, Hq, total_q)
+        lse = _lse(call, lse, return_lse, total_q, Hq, self.device)
+        p = Packed(cu_q.numel() - 1, Hq, k.shape[1], 128, code, int(bool(causal)), total_q, k.shape[0], scale,
+                   q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                   out.stride(0), out.stride(1))
+        need = packed_workspace_bytes(p)
+        with _on(self.device):
+            packed_attention_fwd(p, q, k, v, cu_q, cu_k, out, lse, self._ws.get(need or 256))
+        return (out, lse) if lse is not None else out
+
+    def check(self) -> None:
+        """Synchronises and raises what the calls' kernels reported."""
+        self._ws.check()
+
+
+class _on:
+    """Makes a tensor's device the current one for a call."""
+
+    def __init__(self, device):
+        self.index, self.before = device.index, None
+
+    def __enter__(self):
+        import torch
+        now = torch.cuda.current_device()
+        if now != self.index:
+            self.before = now
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        import torch
+        if self.before is not None:
+            torch.cuda.set_device(self.before)
+
+
+def _lse(call: str, lse, wanted: bool, tokens: int, heads: int, device):
+    import torch
+    if lse is None:
+        return torch.empty((tokens, heads), dtype=torch.float32, device=device) if wanted else None
+    if lse.shape != (tokens, heads) or lse.dtype != torch.float32 or lse.device != device or not lse.is_contiguous():
+        raise _bad(call, f"lse: a contiguous float32 [{tokens}, {heads}] tensor on {device}")
+    return lse
+
+
+class PagedCache:
+    """A paged key/value cache: pool [2, layers, n_pages, Hkv, page_size, 128]
+    (keys, values) and int32 state, owned through PyTorch, with the page
+    operations and the attention over it on the current stream.  Calls of one
+    object must not overlap on the GPU.  `pool` and `state` may be given: a
+    state that describes the pool's contents, e.g. a copy of `.state`.
+    `.refs`, `.lens` and `.table` are views of the state."""
+
+    def __init__(self, layers: int, n_pages: int, page_size: int, Hkv: int, max_seqs: int, max_pages: int,
+                 dtype=None, device="cuda", pool=None, state=None):
+        import torch
+        call = "paged_cache"
+        self.dtype = torch.float16 if dtype is None else dtype
+        self.p = CacheProblem(layers, n_pages, page_size, Hkv, 128, _dtype(call, self.dtype), max_seqs, max_pages)
+        _check("ra_cache_validate", cache_validate(self.p))
+        self.device = torch.empty(0, device=device).device
+        shape = (2, layers, n_pages, Hkv, page_size, 128)
+        ints = cache_state_bytes(self.p) // 4
+        if pool is None:
+            pool = torch.empty(shape, dtype=self.dtype, device=self.device)
+        if pool.shape != shape or pool.dtype != self.dtype or pool.device != self.device or not pool.is_contiguous():
+            raise _bad(call, f"pool: a contiguous {self.dtype} tensor {shape} on {self.device}")
+        fresh = state is None
+        if fresh:
+            state = torch.empty((ints,), dtype=torch.int32, device=self.device)
+        _ints(call, "state", state, self.device, ints)
+        self.pool, self.state = pool, state
+        self.c = cache_bind(self.p, pool, state)
+        at = lambda ptr: (ptr - state.data_ptr()) // 4   # noqa: E731
+        self.refs = state[:n_pages]
+        self.lens = state[at(self.c.lens):at(self.c.lens) + max_seqs]
+        self.table = state[at(self.c.table):at(self.c.table) + max_seqs * max_pages].view(max_seqs, max_pages)
+        self._work = torch.zeros((cache_workspace_bytes(self.p),), dtype=torch.uint8, device=self.device)
+        self._ws = _Workspace(self.device)
+        if fresh:
+            with _on(self.device):
+                cache_init(self.p, self.c)
+
+    def extend(self, seqs, n_new) -> None:
+        """Rows `seqs` grow by `n_new` tokens (int32 device lists; -1 rows are passed over)."""
+        _ints("cache_extend", "seqs", seqs, self.device)
+        _ints("cache_extend", "n_new", n_new, self.device, seqs.numel())
+        with _on(self.device):
+            cache_extend(self.p, self.c, seqs, n_new, self._work)
+
+    def write(self, layer: int, seqs, k, v, cu_new=None) -> None:
+        """The last tokens of rows `seqs` in one layer: k, v [tokens, Hkv, 128];
+        row i gets tokens cu_new[i] to cu_new[i + 1], or token i."""
+        call = "cache_write"
+        _ints(call, "seqs", seqs, self.device)
+        if cu_new is not None:
+            _ints(call, "cu_new", cu_new, self.device, seqs.numel() + 1)
+        _rows(call, "k", k, self.dtype, self.device, self.p.Hkv)
+        _rows(call, "v", v, self.dtype, self.device, self.p.Hkv, k.shape[0])
+        with _on(self.device):
+            cache_write(self.p, self.c, layer, seqs, cu_new, k, v, self._work)
+
+    def fork(self, parents, children) -> None:
+        """Empty rows `children` become copies of rows `parents`, sharing their full pages."""
+        _ints("cache_fork", "parents", parents, self.device)
+        _ints("cache_fork", "children", children, self.device, parents.numel())
+        with _on(self.device):
+            cache_fork(self.p, self.c, parents, children, self._work)
+
+    def free(self, seqs) -> None:
+        """Rows `seqs` become empty."""
+        _ints("cache_free", "seqs", seqs, self.device)
+        with _on(self.device):
+            cache_free(self.p, self.c, seqs, self._work)
+
+    def compact(self) -> None:
+        """Moves the n live pages to the first n places."""
+        with _on(self.device):
+            cache_compact(self.p, self.c, self._work)
+
+    def attention(self, layer: int, q, seqs, cu_q=None, shared: int = 0, scale: float = 0.0, out=None, lse=None,
+                  return_lse: bool = False):
+        """The newest tokens q [total_q, Hq, 128] of rows `seqs` (token i, or
+        tokens cu_q[i] to cu_q[i + 1] of row i) over their sequences, whose
+        first `shared` tokens lie in the same pages.  Returns out, or (out, lse)."""
+        import torch
+        call = "cache_attention"
+        _rows(call, "q", q, self.dtype, self.device)
+        _ints(call, "seqs", seqs, self.device)
+        if cu_q is not None:
+            _ints(call, "cu_q", cu_q, self.device, seqs.numel() + 1)
+        total_q, Hq = q.shape[0], q.shape[1]
+        if out is None:
+            out = torch.empty((total_q, Hq, 128), dtype=self.dtype, device=self.device)
+        else:
+            _rows(call, "out", out, self.dtype, self.device, Hq, total_q)
+        lse = _lse(call, lse, return_lse, total_q, Hq, self.device)
+        a = CacheAttn(seqs.numel(), Hq, total_q, layer, shared, scale, q.stride(0), q.stride(1), out.stride(0),
+                      out.stride(1))
+        need = cache_attention_workspace_bytes(self.p, a)
+        with _on(self.device):
+            cache_attention_fwd(self.p, self.c, a, q, seqs, cu_q, out, lse, self._ws.get(need or 256))
+        return (out, lse) if lse is not None else out
+
+    def check(self) -> None:
+        """Synchronises and raises what the calls' kernels reported."""
+        with _on(self.device):
+            check_device_error(self._work)
+        self._ws.check()
+
 
 class RotateAttention:
     """Owns (through PyTorch) the workspace and the quantised-QKV buffer of one

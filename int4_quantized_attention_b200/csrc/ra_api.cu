@@ -376,6 +376,8 @@ ra_status ra_check_device_error(void* ws, ra_stream stream) {
   if (err.word & ra::DEVERR_WORKSPACE)
     return fail(RA_ERR_WORKSPACE, "workspace not prepared for this problem (site 0x%x)", err.site);
   if (err.word & ra::DEVERR_BOUNDS) return fail(RA_ERR_DEVICE_BOUNDS, "device bounds check (site 0x%x)", err.site);
+  if (err.word & ra::DEVERR_FULL)
+    return fail(RA_ERR_CACHE_FULL, "too few free pages or table entries; nothing was changed (site 0x%x)", err.site);
   return fail(RA_ERR_DEVICE_TIMEOUT, "bounded device wait ran out (site 0x%x)", err.site);
 }
 
@@ -388,6 +390,7 @@ const char* ra_status_string(ra_status s) {
     case RA_ERR_CUDA: return "CUDA error";
     case RA_ERR_DEVICE_TIMEOUT: return "device wait timed out";
     case RA_ERR_DEVICE_BOUNDS: return "device bounds check failed";
+    case RA_ERR_CACHE_FULL: return "cache full";
   }
   return "unknown status";
 }

@@ -1,0 +1,442 @@
+// ra_cache.cu -- the pages of a key/value cache: giving pages to sequences
+// that grow, writing new tokens into them, sharing them between sequences
+// (fork), returning them (free) and moving the live ones together (compact).
+//
+// State: refs[page] = number of table entries that name the page (0: free),
+// lens[row] = tokens of the sequence in that row, table[row][0 .. ceil(len /
+// page_size)) = its pages, -1 behind them.  All of it is device memory and
+// changes in stream order, so a captured graph may hold these calls.
+//   - A page is given out lowest number first, in the order of the call's list.
+//   - A part-filled last page belongs to one sequence alone: fork shares the
+//     full pages and copies the filled tokens of the last one.
+//   - compact: with n live pages, the i-th free page below n takes the
+//     contents of the i-th live page at or above n, so as few pages move as
+//     can, and no page is read after it was written.
+//
+// The state part of each call runs on one cluster of 8 CTAs, whose barrier
+// orders its steps (check everything, then change; a call that cannot be
+// carried out changes nothing and reports why).  Counting pages is the only
+// step over all of refs: 4 bytes per page.  The bytes themselves are moved by
+// copy_kernel over the whole GPU from a list of (source, destination, tokens).
+// A step's results depend on the lists and on prefix sums only, not on the
+// order in which threads get there.
+#include <cstdint>
+
+#include "ra_cache.h"
+
+namespace ra {
+namespace {
+
+constexpr int CL = 8;              // CTAs of the state cluster
+constexpr int CT = 1024;           // threads per CTA of it
+constexpr int ALL = CL * CT;
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int ctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return (int)r;
+}
+__device__ __forceinline__ int read_peer(const int* p, int rank) {
+  uint32_t a;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+struct Shared {
+  int warp[32];
+  int total;
+  int bad;
+  int cta[CL];
+};
+
+// Exclusive prefix of x over the cluster's threads, in thread order of CTA 0,
+// 1, ...; `all` gets the total.  Every thread of the cluster calls it.
+__device__ int cluster_prefix(int x, Shared* sh, int& all) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int incl = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += y;
+  }
+  if (lane == 31) sh->warp[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const int v = sh->warp[lane];
+    int run = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, run, d);
+      if (lane >= d) run += y;
+    }
+    sh->warp[lane] = run - v;
+    if (lane == 31) sh->total = run;
+  }
+  cluster_barrier();
+  if (tid < CL) sh->cta[tid] = read_peer(&sh->total, tid);
+  cluster_barrier();   // no CTA reuses `total`, nor ends, before every peer has read it
+  int base = 0;
+  all = 0;
+#pragma unroll
+  for (int c = 0; c < CL; ++c) {
+    if (c < ctarank()) base += sh->cta[c];
+    all += sh->cta[c];
+  }
+  const int out = base + sh->warp[warp] + incl - x;
+  __syncthreads();
+  return out;
+}
+
+// Whether any thread of the cluster says so; all threads call it.
+__device__ bool cluster_any(bool x, Shared* sh) {
+  int all;
+  cluster_prefix(x ? 1 : 0, sh, all);
+  return all != 0;
+}
+
+struct Ws {
+  WsHeader* hdr;
+  int *jobs, *mark, *rank, *list, *map, *src, *dst, *rows;
+};
+__host__ Ws ws_of(const CacheProb& c, void* ws) {
+  const CacheWs L = cache_ws(c.n_pages, c.max_seqs);
+  char* b = static_cast<char*>(ws);
+  auto at = [&](size_t o) { return reinterpret_cast<int*>(b + o); };
+  return {static_cast<WsHeader*>(ws), at(L.jobs), at(L.mark), at(L.rank), at(L.list), at(L.map), at(L.src),
+          at(L.dst), at(L.rows)};
+}
+
+__device__ __forceinline__ int pages_for(const CacheProb& c, int len) { return (len + c.page_size - 1) >> c.page_shift; }
+__device__ __forceinline__ bool row_ok(const CacheProb& c, int row) {
+  if (row < 0 || row >= c.max_seqs) return false;
+  const int len = c.lens[row];
+  return len >= 0 && (long long)len <= (long long)c.max_pages << c.page_shift;
+}
+
+// Marks the rows of a list: rows named twice, or by both lists of a fork, are
+// found by the count.  -1 entries take no part.
+__device__ bool rows_unique(const CacheProb& c, const Ws& w, const int* rows, int n, const int* others, Shared* sh) {
+  const int at = ctarank() * CT + threadIdx.x;
+  for (int i = at; i < n; i += ALL) {
+    if (rows[i] >= 0 && rows[i] < c.max_seqs) w.mark[rows[i]] = 0;
+    if (others != nullptr && others[i] >= 0 && others[i] < c.max_seqs) w.mark[others[i]] = 0;
+  }
+  cluster_barrier();
+  bool bad = false;
+  for (int i = at; i < n; i += ALL) {
+    if (rows[i] == -1) continue;
+    if (!row_ok(c, rows[i])) bad = true;
+    else if (atomicAdd(&w.mark[rows[i]], 1) != 0) bad = true;
+  }
+  cluster_barrier();
+  if (others != nullptr)
+    for (int i = at; i < n; i += ALL) {
+      if (rows[i] == -1) continue;
+      if (!row_ok(c, others[i]) || w.mark[others[i]] != 0) bad = true;
+    }
+  return !cluster_any(bad, sh);
+}
+
+// The first `want` free pages, lowest first, into w.list; false (and nothing
+// changed) if there are fewer.
+__device__ bool lowest_free(const CacheProb& c, const Ws& w, int want, Shared* sh) {
+  const int per = (c.n_pages + ALL - 1) / ALL;
+  const int at = ctarank() * CT + threadIdx.x;
+  const int p0 = min(c.n_pages, at * per), p1 = min(c.n_pages, p0 + per);
+  int free_here = 0;
+  for (int p = p0; p < p1; ++p) free_here += c.refs[p] == 0;
+  int all;
+  int r = cluster_prefix(free_here, sh, all);
+  if (all < want) return false;
+  for (int p = p0; p < p1 && r < want; ++p)
+    if (c.refs[p] == 0) w.list[r++] = p;
+  cluster_barrier();
+  return true;
+}
+
+__device__ __forceinline__ void report_once(WsHeader* h, uint32_t bit, uint32_t site) {
+  if (ctarank() == 0 && threadIdx.x == 0) report(&h->err, bit, site);
+}
+
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
+    extend_kernel(CacheProb c, const int* __restrict__ seqs, const int* __restrict__ n_new, int n, Ws w) {
+  __shared__ Shared sh;
+  if (!rows_unique(c, w, seqs, n, nullptr, &sh)) return report_once(w.hdr, DEVERR_BOUNDS, 0x5001);
+  // entries in list order, a run of consecutive ones per thread
+  const int per = (n + ALL - 1) / ALL, at = ctarank() * CT + threadIdx.x;
+  const int i0 = min(n, at * per), i1 = min(n, i0 + per);
+  int need = 0;
+  bool bad = false, full = false;
+  for (int i = i0; i < i1; ++i) {
+    if (seqs[i] == -1) continue;
+    const int len = c.lens[seqs[i]], add = n_new[i];
+    if (add < 0) {
+      bad = true;
+    } else if ((long long)len + add > (long long)c.max_pages << c.page_shift) {
+      full = true;
+    } else {
+      need += pages_for(c, len + add) - pages_for(c, len);   // summed: at most max_seqs x max_pages < 2^31
+    }
+  }
+  if (cluster_any(bad, &sh)) return report_once(w.hdr, DEVERR_BOUNDS, 0x5002);
+  if (cluster_any(full, &sh)) return report_once(w.hdr, DEVERR_FULL, 0x5003);
+  int want;
+  int r = cluster_prefix(need, &sh, want);
+  if (!lowest_free(c, w, want, &sh)) return report_once(w.hdr, DEVERR_FULL, 0x5004);
+  for (int i = i0; i < i1; ++i) {
+    w.rank[i] = r;
+    if (seqs[i] != -1) r += pages_for(c, c.lens[seqs[i]] + n_new[i]) - pages_for(c, c.lens[seqs[i]]);
+  }
+  cluster_barrier();
+  const int lane = threadIdx.x & 31;
+  for (int i = at >> 5; i < n; i += ALL / 32) {
+    const int row = seqs[i];
+    if (row == -1) continue;
+    const int len = c.lens[row], have = pages_for(c, len), more = pages_for(c, len + n_new[i]) - have, first = w.rank[i];
+    for (int k = lane; k < more; k += 32) {
+      const int page = w.list[first + k];
+      c.table[(long long)row * c.max_pages + have + k] = page;
+      c.refs[page] = 1;
+    }
+    __syncwarp();
+    if (lane == 0) c.lens[row] = len + n_new[i];
+  }
+}
+
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
+    fork_kernel(CacheProb c, const int* __restrict__ parents, const int* __restrict__ children, int n, Ws w) {
+  __shared__ Shared sh;
+  if (ctarank() == 0 && threadIdx.x == 0) w.jobs[0] = 0;   // nothing to copy if this call is refused
+  if (!rows_unique(c, w, children, n, parents, &sh)) return report_once(w.hdr, DEVERR_BOUNDS, 0x5011);
+  const int per = (n + ALL - 1) / ALL, at = ctarank() * CT + threadIdx.x;
+  const int i0 = min(n, at * per), i1 = min(n, i0 + per);
+  int need = 0;
+  bool bad = false;
+  for (int i = i0; i < i1; ++i) {
+    if (children[i] == -1) continue;
+    bad |= c.lens[children[i]] != 0;
+    need += (c.lens[parents[i]] & (c.page_size - 1)) != 0;
+  }
+  if (cluster_any(bad, &sh)) return report_once(w.hdr, DEVERR_BOUNDS, 0x5012);
+  int want;
+  int r = cluster_prefix(need, &sh, want);
+  if (!lowest_free(c, w, want, &sh)) return report_once(w.hdr, DEVERR_FULL, 0x5013);
+  for (int i = i0; i < i1; ++i) {
+    w.rank[i] = r;
+    if (children[i] != -1) r += (c.lens[parents[i]] & (c.page_size - 1)) != 0;
+  }
+  cluster_barrier();
+  const int lane = threadIdx.x & 31;
+  for (int i = at >> 5; i < n; i += ALL / 32) {
+    const int child = children[i];
+    if (child == -1) continue;
+    const int parent = parents[i], len = c.lens[parent], full = len >> c.page_shift, rest = len & (c.page_size - 1);
+    const int* from = c.table + (long long)parent * c.max_pages;
+    int* to = c.table + (long long)child * c.max_pages;
+    for (int k = lane; k < full; k += 32) {
+      const int page = from[k];
+      to[k] = page;
+      if ((uint32_t)page < (uint32_t)c.n_pages) atomicAdd(&c.refs[page], 1);
+      else report(&w.hdr->err, DEVERR_BOUNDS, 0x5014);
+    }
+    if (lane == 0) {
+      if (rest != 0) {
+        const int page = w.list[w.rank[i]], old = from[full];
+        to[full] = page;
+        c.refs[page] = 1;
+        w.src[w.rank[i]] = old;
+        w.dst[w.rank[i]] = page;
+        w.rows[w.rank[i]] = rest;
+        if ((uint32_t)old >= (uint32_t)c.n_pages) {
+          w.rows[w.rank[i]] = 0;
+          report(&w.hdr->err, DEVERR_BOUNDS, 0x5014);
+        }
+      }
+      c.lens[child] = len;
+    }
+  }
+  if (ctarank() == 0 && threadIdx.x == 0) w.jobs[0] = want;
+}
+
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
+    free_kernel(CacheProb c, const int* __restrict__ seqs, int n, Ws w) {
+  __shared__ Shared sh;
+  if (!rows_unique(c, w, seqs, n, nullptr, &sh)) return report_once(w.hdr, DEVERR_BOUNDS, 0x5021);
+  const int lane = threadIdx.x & 31, at = ctarank() * CT + threadIdx.x;
+  for (int i = at >> 5; i < n; i += ALL / 32) {
+    const int row = seqs[i];
+    if (row == -1) continue;
+    const int have = pages_for(c, c.lens[row]);
+    int* t = c.table + (long long)row * c.max_pages;
+    for (int k = lane; k < have; k += 32) {
+      const int page = t[k];
+      if ((uint32_t)page < (uint32_t)c.n_pages) atomicSub(&c.refs[page], 1);
+      else report(&w.hdr->err, DEVERR_BOUNDS, 0x5022);
+      t[k] = -1;
+    }
+    __syncwarp();
+    if (lane == 0) c.lens[row] = 0;
+  }
+}
+
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT) compact_kernel(CacheProb c, Ws w) {
+  __shared__ Shared sh;
+  const int per = (c.n_pages + ALL - 1) / ALL, at = ctarank() * CT + threadIdx.x;
+  const int p0 = min(c.n_pages, at * per), p1 = min(c.n_pages, p0 + per);
+  int live = 0, holes = 0, total;
+  for (int p = p0; p < p1; ++p) live += c.refs[p] > 0;
+  cluster_prefix(live, &sh, total);
+  int movers = 0, n;
+  for (int p = p0; p < p1; ++p) {
+    const bool is = c.refs[p] > 0;
+    holes += !is && p < total;
+    movers += is && p >= total;
+  }
+  int h = cluster_prefix(holes, &sh, n), m = cluster_prefix(movers, &sh, n);
+  for (int p = p0; p < p1; ++p) {
+    const bool is = c.refs[p] > 0;
+    w.map[p] = p;
+    if (!is && p < total) w.dst[h++] = p;
+    if (is && p >= total) w.src[m++] = p;
+  }
+  cluster_barrier();
+  for (int i = at; i < n; i += ALL) {
+    const int from = w.src[i], to = w.dst[i];
+    w.map[from] = to;
+    w.rows[i] = c.page_size;
+    c.refs[to] = c.refs[from];
+    c.refs[from] = 0;
+  }
+  if (at == 0) w.jobs[0] = n;
+}
+
+// Copies the listed pages' tokens in every layer and head: one warp per
+// (page, layer, keys or values, head), a contiguous run of tokens x 256 bytes.
+// Memory-bound: each byte is read once and written once; 8 loads of 16 bytes
+// per lane are in flight before the first store.  With `remap`, the table's
+// entries follow the map as well (a compaction).
+__global__ void __launch_bounds__(256) copy_kernel(CacheProb c, Ws w, int remap) {
+  const int lane = threadIdx.x & 31;
+  const long long warp = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5, warps = (long long)gridDim.x * 8;
+  if (remap) {
+    for (long long row = warp; row < c.max_seqs; row += warps) {
+      if (!row_ok(c, (int)row)) continue;
+      const int have = pages_for(c, c.lens[row]);
+      int* t = c.table + row * c.max_pages;
+      for (int k = lane; k < have; k += 32) {
+        const int page = t[k];
+        if ((uint32_t)page < (uint32_t)c.n_pages) t[k] = w.map[page];
+        else report(&w.hdr->err, DEVERR_BOUNDS, 0x5031);
+      }
+    }
+  }
+  const int per = 2 * c.layers * c.Hkv;
+  const long long runs = (long long)w.jobs[0] * per;
+  const long long head_bytes = (long long)c.page_size * 256, page_bytes = head_bytes * c.Hkv;
+  for (long long run = warp; run < runs; run += warps) {
+    const int job = (int)(run / per), part = (int)(run % per);
+    const int head = part % c.Hkv, layer = (part / c.Hkv) % c.layers;
+    uint8_t* pool = part / c.Hkv >= c.layers ? c.v : c.k;
+    const long long base = (long long)layer * c.n_pages * page_bytes + head * head_bytes;
+    const uint4* src = reinterpret_cast<const uint4*>(pool + base + w.src[job] * page_bytes) + lane;
+    uint4* dst = reinterpret_cast<uint4*>(pool + base + w.dst[job] * page_bytes) + lane;
+    const int chunks = w.rows[job] * 16;   // 16-byte pieces
+    for (int o = 0; o < chunks; o += 256) {
+      uint4 x[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (o + 32 * q + lane < chunks) x[q] = __ldcs(src + o + 32 * q);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (o + 32 * q + lane < chunks) __stcs(dst + o + 32 * q, x[q]);
+    }
+  }
+}
+
+// New tokens into their slots: 16 lanes per (token, head, keys or values).
+__global__ void __launch_bounds__(256)
+    write_kernel(CacheProb c, int layer, const int* __restrict__ seqs, const int* __restrict__ cu_new, int n, int total,
+                 const uint8_t* __restrict__ k, const uint8_t* __restrict__ v, long long k_tok, long long k_head,
+                 long long v_tok, long long v_head, WsHeader* hdr) {
+  const int lane16 = threadIdx.x & 15;
+  const long long unit = ((long long)blockIdx.x * 256 + threadIdx.x) >> 4;
+  const int per = 2 * c.Hkv;
+  if (unit >= (long long)total * per) return;
+  const int t = (int)(unit / per), part = (int)(unit % per), head = part % c.Hkv;
+  const bool is_v = part >= c.Hkv;
+  int i = t, first = t, count = 1;
+  if (cu_new != nullptr) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (cu_new[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    i = lo;
+    first = cu_new[i];
+    count = cu_new[i + 1] - first;
+    if (t < first || t >= first + count) return;   // behind the last sequence
+  }
+  const int row = seqs[i];
+  if (row == -1) return;
+  if (!row_ok(c, row) || c.lens[row] < count) return report(&hdr->err, DEVERR_BOUNDS, 0x5041);
+  const int pos = c.lens[row] - count + (t - first);
+  const int page = c.table[(long long)row * c.max_pages + (pos >> c.page_shift)];
+  if ((uint32_t)page >= (uint32_t)c.n_pages) return report(&hdr->err, DEVERR_BOUNDS, 0x5042);
+  const uint8_t* src = is_v ? v + t * v_tok + head * v_head : k + t * k_tok + head * k_head;
+  const long long slot = (((long long)layer * c.n_pages + page) * c.Hkv + head) * c.page_size + (pos & (c.page_size - 1));
+  reinterpret_cast<uint4*>((is_v ? c.v : c.k) + slot * 256)[lane16] = reinterpret_cast<const uint4*>(src)[lane16];
+}
+
+cudaError_t launch_copy(const CacheProb& c, const Ws& w, int remap, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  copy_kernel<<<8 * sms, 256, 0, st>>>(c, w, remap);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_extend(const CacheProb& c, const int* seqs, const int* n_new, int n, void* ws,
+                                cudaStream_t st) {
+  extend_kernel<<<CL, CT, 0, st>>>(c, seqs, n_new, n, ws_of(c, ws));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_fork(const CacheProb& c, const int* parents, const int* children, int n, void* ws,
+                              cudaStream_t st) {
+  const Ws w = ws_of(c, ws);
+  fork_kernel<<<CL, CT, 0, st>>>(c, parents, children, n, w);
+  cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? launch_copy(c, w, 0, st) : e;
+}
+
+cudaError_t launch_cache_free(const CacheProb& c, const int* seqs, int n, void* ws, cudaStream_t st) {
+  free_kernel<<<CL, CT, 0, st>>>(c, seqs, n, ws_of(c, ws));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_compact(const CacheProb& c, void* ws, cudaStream_t st) {
+  const Ws w = ws_of(c, ws);
+  compact_kernel<<<CL, CT, 0, st>>>(c, w);
+  cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? launch_copy(c, w, 1, st) : e;
+}
+
+cudaError_t launch_cache_write(const CacheProb& c, int layer, const int* seqs, const int* cu_new, int n, int total,
+                               const uint8_t* k, const uint8_t* v, long long k_tok, long long k_head, long long v_tok,
+                               long long v_head, void* ws, cudaStream_t st) {
+  const long long units = (long long)total * 2 * c.Hkv;
+  write_kernel<<<(unsigned)((units * 16 + 255) / 256), 256, 0, st>>>(c, layer, seqs, cu_new, n, total, k, v, k_tok,
+                                                                      k_head, v_tok, v_head,
+                                                                      static_cast<WsHeader*>(ws));
+  return cudaGetLastError();
+}
+
+}  // namespace ra
