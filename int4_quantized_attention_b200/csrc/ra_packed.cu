@@ -51,6 +51,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "ra_serve.h"
 
@@ -64,6 +65,7 @@ static_assert(256 * SOFTMAX_REGS + 128 * ISSUE_REGS <= NUM_THREADS * LAUNCH_REGS
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float RAISE = 8.0f;    // follow the row maximum when it rises by more than this (log2)
 constexpr int NO_TILE = 0x7fffffff;
+constexpr uint32_t POLY_OF_8 = 0x92;   // of 8 pairs of weights, those computed by exp2_poly
 
 struct Smem {
   static constexpr uint32_t QA = 0, QB = 32768;   // 32 KB each: two 16 KB swizzled halves of 64 channels
@@ -75,8 +77,9 @@ struct Smem {
 
 enum : int {
   B_KFULL = 0, B_KEMPTY = 2, B_VFULL = 4, B_VEMPTY = 6, B_QFULL = 8, B_QEMPTY = 9, B_SFULL = 10, B_PFULL = 12,
-  B_ODONE = 14, B_DRAIN = 16, B_SEGFULL = 18, B_SEGEMPTY = 20, NBAR = 22
+  B_ODONE = 16, B_DRAIN = 18, B_TURN = 20, B_SEGFULL = 22, B_SEGEMPTY = 26, NBAR = 30
 };
+constexpr int SEGS = 4;           // segments in flight
 constexpr int SEG_READERS = 11;   // 8 softmax warps, 2 issuers, the V copier
 
 enum : int { OUT_FINAL = 0, OUT_SLOT = 1, OUT_LEAD = 2, OUT_OWN = 3 };
@@ -104,8 +107,8 @@ struct Misc {
   uint64_t bar[NBAR];
   uint32_t tmem;
   int abort_flag;
-  int nf_tile[4];            // per segment (mod 4): first tile with repaired V elements
-  Seg seg[2];
+  int nf_tile[SEGS];         // per segment: first tile with repaired V elements
+  Seg seg[SEGS];
   long long scan[13];
   long long best[13];
   long long total, first_start;
@@ -208,17 +211,22 @@ __device__ __forceinline__ void umma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem
       : "memory");
 }
 
-// K-major operand, K step kk (16 elements) of a tile of two 64-channel halves
-__device__ __forceinline__ uint64_t kmajor_desc(uint32_t base, int kk) {
-  return sw128_desc(base + (kk >> 2) * 16384u + (kk & 3) * 32u);
-}
-// N-major operand: rows (keys) of 128 bytes hold 64 channels, 8-key groups
-// 1024 bytes apart (stride offset), the two 64-channel halves 16384 bytes
-// apart (leading offset); K step kk starts 16 keys on.
-__device__ __forceinline__ uint64_t nmajor_desc(uint32_t base, int kk) {
-  const uint32_t a = base + kk * 2048u;
-  return (uint64_t)((a >> 4) & 0x3FFFu) | ((uint64_t)(16384u >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+// K-major operand tile (two 64-channel halves of 128-byte rows) and the
+// descriptor's step to K step kk (16 channels), both in units of 16 bytes.
+__device__ __forceinline__ uint64_t kmajor_desc(uint32_t base) { return sw128_desc(base); }
+__host__ __device__ constexpr uint64_t kmajor_step(int kk) { return (kk >> 2) * (16384 >> 4) + (kk & 3) * (32 >> 4); }
+// N-major operand tile: rows (keys) of 128 bytes hold 64 channels, 8-key
+// groups 1024 bytes apart (stride offset), the two 64-channel halves 16384
+// bytes apart (leading offset); a K step is 16 keys, 2048 bytes.
+__device__ __forceinline__ uint64_t nmajor_desc(uint32_t base) {
+  return (uint64_t)((base >> 4) & 0x3FFFu) | ((uint64_t)(16384u >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
          ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 template <bool BF16>
@@ -241,6 +249,37 @@ template <bool BF16>
 __device__ __forceinline__ float widen16(uint32_t h) {
   if constexpr (BF16) return __uint_as_float(h << 16);
   return __half2float(__ushort_as_half((unsigned short)h));
+}
+
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 2^x of a pair on the FMA and integer pipes, for x <= 127: n = rne(x) by
+// adding 1.5 2^23, f = x - n in [-1/2, 1/2], 2^f by its minimax polynomial of
+// degree 5 (Remez exchange on the relative error: 7.5e-8, 2.2e-7 with the
+// fp32 roundings), 2^n by adding n to the exponent field.  Below 2^-126 it
+// gives about 2^-126.
+__device__ __forceinline__ void exp2_poly(float& y0, float& y1, float x0, float x1) {
+  constexpr float MAGIC = 12582912.0f;
+  constexpr float C0 = 1.0000001192092896f, C1 = 0.6931469440460205f, C2 = 0.24022120237350464f,
+                  C3 = 0.05550713092088699f, C4 = 0.009675540961325169f, C5 = 0.0013276472454890609f;
+  x0 = fmaxf(x0, -126.0f);
+  x1 = fmaxf(x1, -126.0f);
+  float n0, n1, f0, f1;
+  add2(n0, n1, x0, x1, MAGIC, MAGIC);
+  add2(f0, f1, n0, n1, -MAGIC, -MAGIC);
+  fma2(f0, f1, f0, f1, -1.0f, -1.0f, x0, x1);
+  float p0, p1;
+  fma2(p0, p1, f0, f1, C5, C5, C4, C4);
+  fma2(p0, p1, p0, p1, f0, f1, C3, C3);
+  fma2(p0, p1, p0, p1, f0, f1, C2, C2);
+  fma2(p0, p1, p0, p1, f0, f1, C1, C1);
+  fma2(p0, p1, p0, p1, f0, f1, C0, C0);
+  y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(n0) << 23));
+  y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(n1) << 23));
 }
 
 // ---------------------------------------------------------------- segment list
@@ -449,9 +488,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar[B_SFULL + i], 1);
-      mbar_init(&bar[B_PFULL + i], 4);
+      mbar_init(&bar[B_PFULL + i], 4);       // first half of P, tile A / B
+      mbar_init(&bar[B_PFULL + 2 + i], 4);   // second half
       mbar_init(&bar[B_ODONE + i], 1);
       mbar_init(&bar[B_DRAIN + i], 1);
+      mbar_init(&bar[B_TURN + i], 1);
+    }
+    for (int i = 0; i < SEGS; ++i) {
       mbar_init(&bar[B_SEGFULL + i], 1);
       mbar_init(&bar[B_SEGEMPTY + i], SEG_READERS);
     }
@@ -481,13 +524,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto wait_all = [&](int b, uint32_t parity, uint32_t site) {
     return __all_sync(0xffffffffu, wait(b, parity, site)) != 0;
   };
-  // Segment k, copied by a reader warp, which then frees its place.
-  auto take_segment = [&](int k, Seg& g, uint32_t site) {
-    if (!wait_all(B_SEGFULL + (k & 1), (k >> 1) & 1, site)) return false;
-    g = mi->seg[k & 1];
+  // Segment k, once it is published; a reader warp frees its place when it no
+  // longer reads it.
+  auto segment = [&](int k, uint32_t site) -> const Seg* {
+    return wait_all(B_SEGFULL + k % SEGS, (k / SEGS) & 1, site) ? &mi->seg[k % SEGS] : nullptr;
+  };
+  auto free_segment = [&](int k) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bar[B_SEGEMPTY + (k & 1)]);
-    return true;
+    if (lane == 0) mbar_arrive(&bar[B_SEGEMPTY + k % SEGS]);
   };
 
   if (warp < 8) {
@@ -498,13 +542,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const float cs = P.cs;
     const int rtok = r / P.G, rhead = r % P.G;
     uint32_t s_phase = 0, o_phase = 0;
-    Seg g;
     for (int k = 0;; ++k) {
-      if (!take_segment(k, g, 0x4101) || g.stop) break;
+      const Seg* seg = segment(k, 0x4101);
+      if (seg == nullptr || seg->stop) break;
+      const Seg& g = *seg;
       const int n = X ? g.n[1] : g.n[0];
       const int tt = g.tok + X * P.TQ + rtok;              // token within the sequence (lead: within all)
       const bool valid = rtok < P.TQ && X * P.TQ + rtok < g.ntok;
-      if (X * P.TQ >= g.ntok) continue;                    // no tile B in this item
+      if (X * P.TQ >= g.ntok) {                            // no tile B in this item
+        free_segment(k);
+        continue;
+      }
       // this row's limit, and the smallest of the tile's (the same in its four warps)
       const int t0 = g.tok + X * P.TQ, t1 = min(t0 + P.TQ, g.tok + g.ntok);
       int lim, gmin;
@@ -552,7 +600,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
               for (int e = 0; e < 4; ++e) bad |= nonfinite16<BF16>(x[e] & 0xffffu) || nonfinite16<BF16>(x[e] >> 16);
               if (bad) {
-                atomicMin(&mi->nf_tile[k & 3], g.tile0 + t);
+                atomicMin(&mi->nf_tile[k % SEGS], g.tile0 + t);
                 __threadfence_block();
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -573,23 +621,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
           tmem_wait_ld();
           const int nvalid = lim - key;
-          if (__any_sync(0xffffffffu, nvalid < KEYS)) {
+          const bool masked = __any_sync(0xffffffffu, nvalid < KEYS);
+          if (masked) {
 #pragma unroll
             for (int e = 0; e < 128; ++e)
               if (e >= nvalid) s[e] = 0xFF800000u;   // -inf: out of the max and the sum
           }
+          // a NaN score makes the maximum, and so the row, NaN
           float mh[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            mh[c] = fmax3(__uint_as_float(s[16 * c]), __uint_as_float(s[16 * c + 1]), __uint_as_float(s[16 * c + 2]));
+            mh[c] = max3_nan(__uint_as_float(s[16 * c]), __uint_as_float(s[16 * c + 1]), __uint_as_float(s[16 * c + 2]));
 #pragma unroll
             for (int e = 3; e < 15; e += 2)
-              mh[c] = fmax3(mh[c], __uint_as_float(s[16 * c + e]), __uint_as_float(s[16 * c + e + 1]));
-            mh[c] = fmaxf(mh[c], __uint_as_float(s[16 * c + 15]));
+              mh[c] = max3_nan(mh[c], __uint_as_float(s[16 * c + e]), __uint_as_float(s[16 * c + e + 1]));
           }
-          const float mx = fmaxf(fmaxf(fmax3(mh[0], mh[1], mh[2]), fmax3(mh[3], mh[4], mh[5])), fmaxf(mh[6], mh[7])) * cs;
-          const bool moved = mx > m + RAISE;           // from -inf: as soon as a key is seen
-          const float m_new = moved ? mx : m;
+#pragma unroll
+          for (int c = 0; c < 8; c += 2)
+            mh[c] = max3_nan(max3_nan(mh[c], mh[c + 1], __uint_as_float(s[16 * c + 15])), __uint_as_float(s[16 * c + 31]), mh[c]);
+          const float mx = max3_nan(max3_nan(mh[0], mh[2], mh[4]), mh[6], mh[6]) * cs;
+          const bool moved = !(mx <= m + RAISE);       // from -inf: as soon as a key is seen
+          const float m_new = moved ? (mx == INFINITY ? NAN : mx) : m;   // an infinite score: inf - inf
           const float alpha = moved ? ex2(m - m_new) : 1.0f;
           m = m_new;
           const float add = BIAS - (m == -INFINITY ? 0.0f : m);
@@ -607,30 +659,54 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
           }
           float l0 = 0.0f, l1 = 0.0f;
-          uint32_t ph[64];
+          // P in two halves: the first one's product starts under the second one's exponentials
+          auto weights = [&](auto poly, int half) {
+            uint32_t ph[32];
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            float x0, x1;
-            fma2(x0, x1, __uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]), cs, cs, add, add);
-            const float p0 = ex2(x0), p1 = ex2(x1);
-            add2(l0, l1, l0, l1, p0, p1);
-            ph[c] = pack2<BF16>(p0, p1);
+            for (int c = 0; c < 32; ++c) {
+              const int e = 64 * half + 2 * c;
+              float x0, x1, p0, p1;
+              fma2(x0, x1, __uint_as_float(s[e]), __uint_as_float(s[e + 1]), cs, cs, add, add);
+              if (decltype(poly)::value && POLY_OF_8 >> (c & 7) & 1) {
+                exp2_poly(p0, p1, x0, x1);
+              } else {
+                p0 = ex2(x0);
+                p1 = ex2(x1);
+              }
+              add2(l0, l1, l0, l1, p0, p1);
+              ph[c] = pack2<BF16>(p0, p1);
+            }
+            tmem_st32(tS + 64 + 32 * half, ph);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[B_PFULL + 2 * half + X]);
+          };
+          if (masked) {
+            weights(std::false_type(), 0);
+            weights(std::false_type(), 1);
+          } else {
+            weights(std::true_type(), 0);
+            weights(std::true_type(), 1);
           }
           l = fmaf(l, alpha, l0 + l1);
-          tmem_st32(tS + 64, ph);
-          tmem_st32(tS + 96, ph + 32);
-          tmem_wait_st();
-          tc_fence_before();
+        } else {
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bar[B_PFULL + X]);
+            mbar_arrive(&bar[B_PFULL + 2 + X]);
+          }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[B_PFULL + X]);
       }
       if (!ok) break;
       if (n > 0) {
         if (!wait_all(B_ODONE + X, o_phase & 1, 0x4104)) break;
         ++o_phase;
       }
-      if (!active) continue;
+      if (!active) {
+        free_segment(k);
+        continue;
+      }
       // epilogue: rows of this segment, final or partial
       tc_fence_after();
       const float inv = l != 0.0f ? 1.0f / l : 0.0f;
@@ -638,7 +714,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int token = g.q0 + tt, head = g.kvh * P.G + rhead;
       const bool store = valid && in_bounds(token >= 0 && token < P.total_q && head < P.Hq, err, 0x4105);
       const long long grow = (long long)token * P.Hq + head;
-      const int nf = *reinterpret_cast<volatile int*>(&mi->nf_tile[k & 3]);
+      const int nf = *reinterpret_cast<volatile int*>(&mi->nf_tile[k % SEGS]);
       float* frow = nullptr;
       uint8_t* hrow = nullptr;
       if (g.out == OUT_FINAL) {
@@ -694,6 +770,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       tc_fence_before();   // O has been read: the next segment's first P.V follows this row's next P
+      free_segment(k);
     }
   } else if (warp == 8 || warp == 11) {
     // ------------------------------------------------------------ copies
@@ -725,12 +802,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         next_segment(P, mi, w, g, err);
         g.ring = ring;
         g.qidx = qidx;
-        if (k >= 2 && !(ok = wait_all(B_SEGEMPTY + (k & 1), ((k >> 1) - 1) & 1, 0x4201))) break;
+        if (k >= SEGS && !(ok = wait_all(B_SEGEMPTY + k % SEGS, (k / SEGS - 1) & 1, 0x4201))) break;
         if (lane == 0) {
-          mi->seg[k & 1] = g;
-          mi->nf_tile[k & 3] = NO_TILE;
+          mi->seg[k % SEGS] = g;
+          mi->nf_tile[k % SEGS] = NO_TILE;
           __threadfence_block();
-          mbar_arrive(&bar[B_SEGFULL + (k & 1)]);
+          mbar_arrive(&bar[B_SEGFULL + k % SEGS]);
         }
         __syncwarp();
         if (g.stop) break;
@@ -748,7 +825,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ++qidx;
         }
       } else {
-        if (!(ok = take_segment(k, g, 0x4203)) || g.stop) break;
+        const Seg* seg = segment(k, 0x4203);
+        if (!(ok = seg != nullptr)) break;
+        g = *seg;
+        free_segment(k);
+        if (g.stop) break;
       }
       for (int t = 0; t < g.nload; ++t, ++ring) {
         const int st = ring % STAGES;
@@ -792,76 +873,110 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_wait(&bar[FULL + t % STAGES], (t / STAGES) & 1, limit_ns, err, 0x4207);
   } else {
     // ------------------------------------------------------------ MMA issuers
-    const int X = warp - 9;
-    const uint32_t qa = smem_u32(sm + (X ? Smem::QB : Smem::QA));
-    const uint32_t kb = smem_u32(sm + Smem::K), vb = smem_u32(sm + Smem::V);
-    const uint32_t tS = tbase + X * 128, tO = tbase + 256 + X * 128;
+    // One warp per query tile.  They take turns, tile A's P.V(t) and S(t+1),
+    // then tile B's: so the tiles stay half a period apart and one tile's
+    // softmax runs under the other's products.  (Without turns the two fall
+    // into step, both in the exponentials, sharing their pipe, then both
+    // waiting; one warp for both adds its own waits to the critical path.)
+    // The warp stays converged and its addresses uniform (one elected lane
+    // issues): descriptors live in uniform registers and step by additions,
+    // where a lane of its own took ~100 cycles per MMA to move them there.
+    const int X = __shfl_sync(0xffffffffu, warp - 9, 0);
+    const uint64_t qd = kmajor_desc(smem_u32(sm + Smem::QA)) + X * (32768 >> 4);
+    const uint64_t kd = kmajor_desc(smem_u32(sm + Smem::K)), vd = nmajor_desc(smem_u32(sm + Smem::V));
+    const uint32_t tS = __shfl_sync(0xffffffffu, tbase, 0) + X * 128, tO = tS + 256;
     uint32_t p_phase = 0;
-    Seg g;
-    for (int k = 0;; ++k) {
-      if (!take_segment(k, g, 0x4301) || g.stop) break;
-      if (g.nload == 0) continue;
-      int ok = 1;
-      if (lane == 0) {
-        const int n = X ? g.n[1] : g.n[0];
-        auto issue_S = [&](int t) {   // S(t) = Q K(t)^T, then release the K stage
-          const int ring = g.ring + t;
-          const uint32_t kt = kb + (ring % STAGES) * 32768;
+    int turn = 0;                  // groups of this tile so far
+    auto spin_all = [&](int b, uint32_t parity, uint32_t site) {
+      // polls without suspending at first, then as every other wait
+#pragma unroll 1
+      for (int i = 0; i < 64; ++i)
+        if (__all_sync(0xffffffffu, mbar_test_wait(&bar[b], parity))) return true;
+      return wait_all(b, parity, site);
+    };
+    auto issue_S = [&](int ring) {   // S = Q K^T
+      const uint64_t kt = kd + (ring % STAGES) * (32768 >> 4);
+      if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) umma_f16(tS, kmajor_desc(qa, kk), kmajor_desc(kt, kk), IDESC_S, kk > 0);
-          umma_commit(&bar[B_SFULL + X]);
-          umma_commit(&bar[B_KEMPTY + ring % STAGES]);
-          if (t == n - 1) umma_commit(&bar[B_QEMPTY]);
-        };
-        auto k_full = [&](int t) {
-          const int ring = g.ring + t;
-          return wait(B_KFULL + ring % STAGES, (ring / STAGES) & 1, 0x4302);
-        };
-        auto v_full = [&](int t) {
-          const int ring = g.ring + t;
-          return wait(B_VFULL + ring % STAGES, (ring / STAGES) & 1, 0x4303);
-        };
-        ok = wait(B_QFULL, g.qidx & 1, 0x4304);
-        if (ok && n == 0) mbar_arrive(&bar[B_QEMPTY]);
-        if (ok && n > 0 && (ok = k_full(0))) {
-          tc_fence_after();
-          issue_S(0);
-        }
-        for (int t = 0; ok && t < n; ++t) {
-          if (!(ok = wait(B_PFULL + X, p_phase & 1, 0x4305))) break;
-          ++p_phase;
-          if (!(ok = v_full(t))) break;
-          tc_fence_after();
-          const int ring = g.ring + t;
-          const uint32_t vt = vb + (ring % STAGES) * 32768;   // O += P(t) V(t), P from TMEM
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_f16_tmem_a(tO, tS + 64 + 8 * kk, nmajor_desc(vt, kk), IDESC_PV, (t > 0) || (kk > 0));
-          umma_commit(&bar[B_VEMPTY + ring % STAGES]);
-          if (t + 1 < n) {
-            if (!(ok = k_full(t + 1))) break;
-            tc_fence_after();
-            issue_S(t + 1);
-          } else {
-            umma_commit(&bar[B_ODONE + X]);
+        for (int kk = 0; kk < 8; ++kk)
+          umma_f16(tS, qd + kmajor_step(kk), kt + kmajor_step(kk), IDESC_S, kk > 0);
+        umma_commit(&bar[B_SFULL + X]);
+      }
+      __syncwarp();
+    };
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const Seg* seg = segment(k, 0x4301);
+      if (!(ok = seg != nullptr)) break;
+      const Seg& g = *seg;
+      const int nload = __shfl_sync(0xffffffffu, g.nload, 0), ring0 = __shfl_sync(0xffffffffu, g.ring, 0);
+      const int n = __shfl_sync(0xffffffffu, X ? g.n[1] : g.n[0], 0);
+      const int q_phase = __shfl_sync(0xffffffffu, g.qidx & 1, 0), stop = __shfl_sync(0xffffffffu, g.stop, 0);
+      free_segment(k);
+      if (stop) break;
+      if (nload == 0) continue;
+      auto k_full = [&](int t) {
+        return wait_all(B_KFULL + (ring0 + t) % STAGES, ((ring0 + t) / STAGES) & 1, 0x4302);
+      };
+      auto k_done = [&](int t, bool mma) {   // this tile's S has read K(t), or never will
+        if (elect_one()) {
+          if (mma) umma_commit(&bar[B_KEMPTY + (ring0 + t) % STAGES]);
+          else mbar_arrive(&bar[B_KEMPTY + (ring0 + t) % STAGES]);
+          if (t == nload - 1) {
+            if (mma) umma_commit(&bar[B_QEMPTY]);
+            else mbar_arrive(&bar[B_QEMPTY]);
           }
         }
-        // tiles that only the other query tile needs
-        for (int t = n; ok && t < g.nload; ++t) {
-          const int ring = g.ring + t;
-          if (!(ok = k_full(t))) break;
-          mbar_arrive(&bar[B_KEMPTY + ring % STAGES]);
-          if (!(ok = v_full(t))) break;
-          mbar_arrive(&bar[B_VEMPTY + ring % STAGES]);
+        __syncwarp();
+      };
+      if (!(ok = wait_all(B_QFULL, q_phase, 0x4304) && k_full(0))) break;
+      tc_fence_after();
+      if (n > 0) issue_S(ring0);
+      k_done(0, n > 0);
+      for (int t = 0; t < nload; ++t) {
+        const int ring = ring0 + t;
+        const uint64_t vt = vd + (ring % STAGES) * (32768 >> 4);
+        if (!(ok = wait_all(B_VFULL + ring % STAGES, (ring / STAGES) & 1, 0x4303))) break;
+        if (t + 1 < nload && !(ok = k_full(t + 1))) break;
+        // A goes first; its first turn needs no leave
+        if (X == 1 || turn > 0) {
+          if (!(ok = spin_all(B_TURN + X, (X ? turn : turn - 1) & 1, 0x4306))) break;
         }
+        ++turn;
+        if (t < n) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {   // O += P(t) V(t), P from TMEM
+            if (!ok || !(ok = spin_all(B_PFULL + 2 * half + X, p_phase, 0x4305))) continue;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                umma_f16_tmem_a(tO, tS + 64 + 8 * kk, vt + kk * (2048 >> 4), IDESC_PV, (t > 0) || (kk > 0));
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          p_phase ^= 1u;
+          if (t + 1 < n) {
+            issue_S(ring + 1);
+          } else {
+            if (elect_one()) umma_commit(&bar[B_ODONE + X]);
+            __syncwarp();
+          }
+        }
+        if (lane == 0) mbar_arrive(&bar[B_TURN + 1 - X]);
+        __syncwarp();
+        if (elect_one()) {
+          if (t < n) umma_commit(&bar[B_VEMPTY + ring % STAGES]);
+          else mbar_arrive(&bar[B_VEMPTY + ring % STAGES]);
+        }
+        __syncwarp();
+        if (t + 1 < nload) k_done(t + 1, t + 1 < n);
       }
-      p_phase = __shfl_sync(0xffffffffu, p_phase, 0);
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
     }
-    if (lane == 0) {   // every MMA this thread issued completes before TMEM is released
-      umma_commit(&bar[B_DRAIN + X]);
-      mbar_wait(&bar[B_DRAIN + X], 0, limit_ns, err, 0x4306);
-    }
+    if (elect_one()) umma_commit(&bar[B_DRAIN + X]);   // every MMA completes before TMEM is released
+    __syncwarp();
+    mbar_wait(&bar[B_DRAIN + X], 0, limit_ns, err, 0x4306);
   }
   tc_fence_before();
   __syncthreads();
