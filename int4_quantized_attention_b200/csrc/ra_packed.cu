@@ -15,8 +15,8 @@
 //
 // Every CTA is persistent (one per SM) and walks a list of segments: (item,
 // range of 128-key tiles).  Two ways to deal them out:
-//   whole items  CTA c takes items c, c + grid, ...; the last (longest) query
-//                tiles of each sequence come first.  Rows are final.
+//   whole items  one item per CTA in rounds, there and back; the last (longest)
+//                query tiles of each sequence come first.  Rows are final.
 //   split        all key tiles of all items, laid end to end, are cut into
 //                equal shares, one per CTA, whatever the lengths are; an item
 //                that crosses a border leaves partial rows (fp32) that
@@ -51,7 +51,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
-#include <type_traits>
 
 #include "ra_serve.h"
 
@@ -65,7 +64,6 @@ static_assert(256 * SOFTMAX_REGS + 128 * ISSUE_REGS <= NUM_THREADS * LAUNCH_REGS
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float RAISE = 8.0f;    // follow the row maximum when it rises by more than this (log2)
 constexpr int NO_TILE = 0x7fffffff;
-constexpr uint32_t POLY_OF_8 = 0x92;   // of 8 pairs of weights, those computed by exp2_poly
 
 struct Smem {
   static constexpr uint32_t QA = 0, QB = 32768;   // 32 KB each: two 16 KB swizzled halves of 64 channels
@@ -257,36 +255,11 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   return r;
 }
 
-// 2^x of a pair on the FMA and integer pipes, for x <= 127: n = rne(x) by
-// adding 1.5 2^23, f = x - n in [-1/2, 1/2], 2^f by its minimax polynomial of
-// degree 5 (Remez exchange on the relative error: 7.5e-8, 2.2e-7 with the
-// fp32 roundings), 2^n by adding n to the exponent field.  Below 2^-126 it
-// gives about 2^-126.
-__device__ __forceinline__ void exp2_poly(float& y0, float& y1, float x0, float x1) {
-  constexpr float MAGIC = 12582912.0f;
-  constexpr float C0 = 1.0000001192092896f, C1 = 0.6931469440460205f, C2 = 0.24022120237350464f,
-                  C3 = 0.05550713092088699f, C4 = 0.009675540961325169f, C5 = 0.0013276472454890609f;
-  x0 = fmaxf(x0, -126.0f);
-  x1 = fmaxf(x1, -126.0f);
-  float n0, n1, f0, f1;
-  add2(n0, n1, x0, x1, MAGIC, MAGIC);
-  add2(f0, f1, n0, n1, -MAGIC, -MAGIC);
-  fma2(f0, f1, f0, f1, -1.0f, -1.0f, x0, x1);
-  float p0, p1;
-  fma2(p0, p1, f0, f1, C5, C5, C4, C4);
-  fma2(p0, p1, p0, p1, f0, f1, C3, C3);
-  fma2(p0, p1, p0, p1, f0, f1, C2, C2);
-  fma2(p0, p1, p0, p1, f0, f1, C1, C1);
-  fma2(p0, p1, p0, p1, f0, f1, C0, C0);
-  y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(n0) << 23));
-  y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(n1) << 23));
-}
-
 // ---------------------------------------------------------------- segment list
 // The list warp's walk; every lane holds the same values.
 struct Walk {
-  long long at, end;     // split: tiles of this CTA's share still to come; whole: item index, stride in `end`
-  int seq;               // split: sequence that `at` lies in
+  long long at, end;     // split: tiles of this CTA's share still to come; whole: first item of the next round
+  int seq;               // split: sequence that `at` lies in; whole: round
   long long start;       // split: its first tile
 };
 
@@ -312,9 +285,14 @@ __device__ __forceinline__ void next_segment(const SeqProb& P, const Misc* mi, W
   if (!P.split) {
     const int per = 2 * P.TQ;
     while (w.at < P.items) {
-      const long long pr = P.items / P.Hkv - 1 - w.at / P.Hkv;
-      g.kvh = (int)(w.at % P.Hkv);
-      w.at += w.end;
+      // rounds of one item per CTA, every other one backwards: items get
+      // shorter along the list, and this evens out what each CTA gets
+      const long long item = w.at + (w.seq & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      w.at += gridDim.x;
+      ++w.seq;
+      if (item >= P.items) continue;
+      const long long pr = P.items / P.Hkv - 1 - item / P.Hkv;
+      g.kvh = (int)(item % P.Hkv);
       // sequence i's pairs lie at cu_q[i] / per + i and on (never more than
       // the gap to the next sequence's first)
       int lo = 0, hi = P.n_seqs - 1;
@@ -621,8 +599,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
           tmem_wait_ld();
           const int nvalid = lim - key;
-          const bool masked = __any_sync(0xffffffffu, nvalid < KEYS);
-          if (masked) {
+          if (__any_sync(0xffffffffu, nvalid < KEYS)) {
 #pragma unroll
             for (int e = 0; e < 128; ++e)
               if (e >= nvalid) s[e] = 0xFF800000u;   // -inf: out of the max and the sum
@@ -660,19 +637,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           float l0 = 0.0f, l1 = 0.0f;
           // P in two halves: the first one's product starts under the second one's exponentials
-          auto weights = [&](auto poly, int half) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
             uint32_t ph[32];
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
               const int e = 64 * half + 2 * c;
-              float x0, x1, p0, p1;
+              float x0, x1;
               fma2(x0, x1, __uint_as_float(s[e]), __uint_as_float(s[e + 1]), cs, cs, add, add);
-              if (decltype(poly)::value && POLY_OF_8 >> (c & 7) & 1) {
-                exp2_poly(p0, p1, x0, x1);
-              } else {
-                p0 = ex2(x0);
-                p1 = ex2(x1);
-              }
+              const float p0 = ex2(x0), p1 = ex2(x1);
               add2(l0, l1, l0, l1, p0, p1);
               ph[c] = pack2<BF16>(p0, p1);
             }
@@ -681,13 +654,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[B_PFULL + 2 * half + X]);
-          };
-          if (masked) {
-            weights(std::false_type(), 0);
-            weights(std::false_type(), 1);
-          } else {
-            weights(std::true_type(), 0);
-            weights(std::true_type(), 1);
           }
           l = fmaf(l, alpha, l0 + l1);
         } else {
@@ -789,10 +755,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       w.seq = mi->first_seq;
       w.start = mi->first_start;
     } else {
-      w.at = blockIdx.x;
-      w.end = gridDim.x;
+      w.at = w.end = w.start = 0;
       w.seq = 0;
-      w.start = 0;
     }
     int ring = 0, qidx = 0;
     bool ok = true;
