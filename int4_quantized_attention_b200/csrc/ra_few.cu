@@ -1,0 +1,309 @@
+// ra_few.cu -- attention of at most 64 query rows (a token, or a few, of one
+// sequence, with the query heads that share a key head) over the pages of a
+// cache: the decoding step.
+//
+// Mathematics: as ra_packed.cu, o = sum_j p_j v_j / sum_j p_j.  Each K and V
+// element is used by 1 to 64 rows only, so the pages' bytes set the pace (512
+// bytes per token and key head), not the products.  Hence
+//   - three small CTAs per SM rather than one large pipeline: what one waits
+//     for (page numbers, the join of its warps, the first tile of its next
+//     item), the others hide;
+//   - the warp-level MMA (m16n8k16): 16 rows cost 32 of them per 16 keys, where
+//     a tensor-memory tile would be 128 rows high and its softmax would have
+//     to go through them;
+//   - K and V tiles of 64 keys by 16-byte asynchronous copies, which fetch any
+//     page layout at the same cost and fill slots past the region's end with
+//     zeros, so that what lies there (NaN, say) never reaches a product.
+//
+// A CTA's four warps share the tile's keys: with R 16-row blocks of queries (R
+// = 1, 2, 4), warp w works for block w % R on keys 16 R (w / R) .. + 16 R - 1,
+// 16 at a time, with a running maximum, sum and fp32 accumulator of its own; the
+// 4 / R partial results of each row are joined through shared memory at the
+// end of the part.  The work is dealt as in the split form of ra_packed.cu:
+// equal shares of all tiles, parts of an item joined by the combine kernel.
+#include "ra_seq.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int THREADS = 128;
+constexpr uint32_t HALF_STAGE = FEW_KEYS * 256;       // K or V of a tile: 16 KB
+constexpr uint32_t RING = 2 * 2 * HALF_STAGE;         // two stages; afterwards the warps' rows, 4 x 16 x 512 bytes
+constexpr int NO_COPY = 0x1ffffff;                    // a tile past every region's end
+static_assert(RING >= 4 * 16 * D * sizeof(float), "join space");
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 16-byte piece c (of 16) of 256-byte row r of a tile: the low three bits of
+// the piece are XORed with the row, so that eight rows of one piece lie in
+// eight different places of the 128-byte bank line.
+__device__ __forceinline__ uint32_t tile_off(uint32_t r, uint32_t c) { return r * 256u + ((c ^ (r & 7u)) << 4); }
+
+template <bool BF16>
+__global__ void __launch_bounds__(THREADS, FEW_CTAS) few_kernel(const __grid_constant__ SeqProb P, WsHeader* __restrict__ hdr) {
+  constexpr float BIAS = BF16 ? 0.0f : 7.0f;   // fp16 weights carry a factor 2^7
+  extern __shared__ __align__(1024) uint8_t sm[];
+  __shared__ SharePlan plan;
+  __shared__ float stat_m[4][16], stat_l[4][16];   // per warp and row of its block
+  __shared__ int nf_tile;                           // first tile with values taken out of V
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  DeviceErr* err = &hdr->err;
+  plan_shares<KIND_FEW, THREADS>(P, plan, err);
+  ShareWalk w;
+  start_walk<KIND_FEW>(P, plan, w);
+  const uint32_t ring = smem_u32(sm);
+  const int copy_row = tid >> 4, copy_piece = tid & 15;   // this thread's rows of a tile: copy_row + 8 i
+  SharePart part;
+  while (next_share_part<KIND_FEW>(P, w, part, err)) {
+    const int rows = part.tokens * P.G, n = part.t1 - part.t0;
+    const int blocks = rows <= 16 ? 1 : rows <= 32 ? 2 : 4, groups = 4 / blocks;
+    const int block = warp & (blocks - 1), group = warp >> (blocks >> 1);
+    const int q0 = part.lead ? 0 : w.s.q0, table_row = part.lead ? plan.lead_row : w.s.row;
+    const int key0 = part.lead ? 0 : P.shared, off = part.lead ? 0 : w.s.off;
+    const int len = part.lead ? min(P.shared, plan.lead_len) : w.s.len;
+    const long long head_off = (long long)part.kvh * P.v_head;
+    const int* pages = P.table + (long long)table_row * P.max_pages;
+    // K and V of tile t (of the region), this thread's 2 x 8 pieces
+    auto copy_tile = [&](int t, int stage) {
+      const uint32_t k_dst = ring + stage * 2 * HALF_STAGE, v_dst = k_dst + HALF_STAGE;
+      int page = -1, slot = -1;
+#pragma unroll
+      for (int i = 0; i < FEW_KEYS / 8; ++i) {
+        const int r = copy_row + 8 * i, key = t * FEW_KEYS + r, pos = key0 + key;
+        bool there = key < len;
+        if (there && (pos >> P.page_shift) != slot) {
+          slot = pos >> P.page_shift;
+          page = __ldg(pages + slot);
+          if ((uint32_t)page >= (uint32_t)P.n_pages) {   // not a page: read as zeros
+            report(err, DEVERR_BOUNDS, 0x4501);
+            page = -1;
+          }
+        }
+        there = there && page >= 0;
+        const long long at = there ? page * P.v_page + head_off + (pos & (P.page_size - 1)) * 256 + copy_piece * 16 : 0;
+        copy16(k_dst + tile_off(r, copy_piece), P.k + at, there);
+        copy16(v_dst + tile_off(r, copy_piece), P.v + at, there);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (tid == 0) nf_tile = NO_TILE;
+    copy_tile(part.t0, 0);
+    copy_tile(n > 1 ? part.t0 + 1 : NO_COPY, 1);   // past the part's end: nothing, but a group all the same
+    // this warp's 16 rows of Q as operand registers; rows past the last are zero
+    uint32_t q[8][4];
+    int lim[2], gmin = len;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 16 * block + 8 * i + (lane >> 2), t = over_G(P, min(r, rows - 1));
+      const bool real = r < rows;
+      const uint8_t* src = P.q + (q0 + t) * P.q_tok + (part.kvh * P.G + min(r, rows - 1) - t * P.G) * P.q_head + 4 * (lane & 3);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        q[kk][i] = real ? *reinterpret_cast<const uint32_t*>(src + 32 * kk) : 0u;
+        q[kk][2 + i] = real ? *reinterpret_cast<const uint32_t*>(src + 32 * kk + 16) : 0u;
+      }
+      lim[i] = real ? row_limit(P, part.lead, off, len, t) : 0;
+    }
+    // keys that every row sees: the first row's, or the least of all of them
+    if (part.lead) {
+      for (int t = lane; t < part.tokens; t += 32) gmin = min(gmin, lead_limit(P, len, t));
+      gmin = __reduce_min_sync(0xffffffffu, gmin);
+    } else {
+      gmin = row_limit(P, 0, off, len, 0);
+    }
+    float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[c][e] = 0.0f;
+
+#pragma unroll 1
+    for (int t = 0; t < n; ++t) {
+      const int key = (part.t0 + t) * FEW_KEYS, stage = t & 1;
+      wait_copies<1>();
+      __syncthreads();
+      const uint32_t kt = ring + stage * 2 * HALF_STAGE, vt = kt + HALF_STAGE;
+      if (key + FEW_KEYS > gmin && gmin < len) {
+        // values that some row must not see meet a zero weight there, and 0 x
+        // infinity is NaN: non-finite ones become zero here, and are added
+        // back at the end for the rows that see them
+        for (int c = tid; c < FEW_KEYS * 16; c += THREADS) {
+          const int r = c >> 4;
+          if (key + r < gmin) continue;
+          uint4* at = reinterpret_cast<uint4*>(sm + (vt - ring) + tile_off(r, c & 15));
+          uint4 v = *at;
+          uint32_t* x = reinterpret_cast<uint32_t*>(&v);
+          bool bad = false;
+          for (int e = 0; e < 4; ++e) {
+            if (nonfinite16<BF16>(x[e])) x[e] &= 0xffff0000u, bad = true;
+            if (nonfinite16<BF16>(x[e] >> 16)) x[e] &= 0xffffu, bad = true;
+          }
+          if (bad) {
+            *at = v;
+            atomicMin(&nf_tile, part.t0 + t);
+          }
+        }
+        __syncthreads();
+      }
+#pragma unroll 1
+      for (int b = 0; b < blocks; ++b) {
+        const int k16 = 16 * (group * blocks + b);   // 16 keys of the tile
+        float s[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        const uint32_t k_row = k16 + (lane & 7) + ((lane >> 4) & 1) * 8;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          uint32_t kf[4];
+          ldmatrix4(kf, kt + tile_off(k_row, 2 * kk + ((lane >> 3) & 1)));
+          mma16816<BF16>(s[0], q[kk], kf[0], kf[1]);
+          mma16816<BF16>(s[1], q[kk], kf[2], kf[3]);
+        }
+        uint32_t p[4];
+        float alpha[2];
+        bool moved[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float x[4] = {s[0][2 * i], s[0][2 * i + 1], s[1][2 * i], s[1][2 * i + 1]};
+          if (key + FEW_KEYS > gmin) {
+            const int first = key + k16 + 2 * (lane & 3);
+            if (first >= lim[i]) x[0] = -INFINITY;
+            if (first + 1 >= lim[i]) x[1] = -INFINITY;
+            if (first + 8 >= lim[i]) x[2] = -INFINITY;
+            if (first + 9 >= lim[i]) x[3] = -INFINITY;
+          }
+          float mx = max3_nan(max3_nan(x[0], x[1], x[2]), x[3], x[3]);
+          float y = __shfl_xor_sync(0xffffffffu, mx, 1);
+          mx = max3_nan(mx, y, y);
+          y = __shfl_xor_sync(0xffffffffu, mx, 2);
+          mx = max3_nan(mx, y, y) * P.cs;
+          moved[i] = !(mx <= m[i] + RAISE);
+          const float m_new = moved[i] ? (mx == INFINITY ? NAN : mx) : m[i];
+          alpha[i] = moved[i] ? ex2(m[i] - m_new) : 1.0f;
+          m[i] = m_new;
+          const float add = BIAS - (m_new == -INFINITY ? 0.0f : m_new);
+          const float p0 = ex2(fmaf(x[0], P.cs, add)), p1 = ex2(fmaf(x[1], P.cs, add));
+          const float p2 = ex2(fmaf(x[2], P.cs, add)), p3 = ex2(fmaf(x[3], P.cs, add));
+          l[i] = fmaf(l[i], alpha[i], (p0 + p1) + (p2 + p3));
+          p[i] = pack2<BF16>(p0, p1);
+          p[2 + i] = pack2<BF16>(p2, p3);
+        }
+        if (__any_sync(0xffffffffu, moved[0] || moved[1])) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            o[c][0] *= alpha[0];
+            o[c][1] *= alpha[0];
+            o[c][2] *= alpha[1];
+            o[c][3] *= alpha[1];
+          }
+        }
+        const uint32_t v_row_ = k16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t vf[4];
+          ldmatrix4_trans(vf, vt + tile_off(v_row_, 2 * c + (lane >> 4)));
+          mma16816<BF16>(o[2 * c], p, vf[0], vf[1]);
+          mma16816<BF16>(o[2 * c + 1], p, vf[2], vf[3]);
+        }
+      }
+      __syncthreads();   // the stage has been read
+      copy_tile(t + 2 < n ? part.t0 + t + 2 : NO_COPY, stage);
+    }
+    wait_copies<0>();
+
+    // join the groups' rows
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float x = l[i];
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      x += __shfl_xor_sync(0xffffffffu, x, 2);
+      if ((lane & 3) == 0) {
+        stat_m[warp][8 * i + (lane >> 2)] = m[i];
+        stat_l[warp][8 * i + (lane >> 2)] = x;
+      }
+    }
+    float* join = reinterpret_cast<float*>(sm);   // [warp][16 rows][128], 16-byte pieces XORed with the row
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const int r = lane >> 2, piece = (2 * c + ((lane >> 1) & 1)) ^ r;
+      float* d = join + (warp * 16 + r) * D + 4 * piece + 2 * (lane & 1);
+      *reinterpret_cast<float2*>(d) = make_float2(o[c][0], o[c][1]);
+      *reinterpret_cast<float2*>(d + 8 * D) = make_float2(o[c][2], o[c][3]);
+    }
+    __syncthreads();
+    const int nf = nf_tile;
+    for (int idx = tid; idx < rows * 16; idx += THREADS) {
+      const int row = idx >> 4, c8 = (idx & 15) * 8, b = row >> 4, r = row & 15;
+      float M = -INFINITY;
+      for (int g = 0; g < groups; ++g) M = max3_nan(M, stat_m[g * blocks + b][r], M);
+      float L = 0.0f, y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      for (int g = 0; g < groups; ++g) {
+        const int v = g * blocks + b;
+        const float f = stat_m[v][r] == -INFINITY ? 0.0f : ex2(stat_m[v][r] - M);
+        L = fmaf(f, stat_l[v][r], L);
+        const float4* x = reinterpret_cast<const float4*>(join + (v * 16 + r) * D);
+        const float4 x0 = x[(c8 / 4) ^ (r & 7)], x1 = x[(c8 / 4 + 1) ^ (r & 7)];
+        y[0] = fmaf(f, x0.x, y[0]);
+        y[1] = fmaf(f, x0.y, y[1]);
+        y[2] = fmaf(f, x0.z, y[2]);
+        y[3] = fmaf(f, x0.w, y[3]);
+        y[4] = fmaf(f, x1.x, y[4]);
+        y[5] = fmaf(f, x1.y, y[5]);
+        y[6] = fmaf(f, x1.z, y[6]);
+        y[7] = fmaf(f, x1.w, y[7]);
+      }
+      const float inv = 1.0f / L;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = L != 0.0f ? y[e] * inv : 0.0f;   // a row without keys; NaN stays
+      const int t = over_G(P, row), token = q0 + t, head = part.kvh * P.G + row - t * P.G;
+      if (nf != NO_TILE)
+        add_nonfinite<BF16, 8>(P, {key0, table_row, part.kvh}, nf * FEW_KEYS,
+                               min(row_limit(P, part.lead, off, len, t), part.t1 * FEW_KEYS), c8, y);
+      if (!in_bounds(token < P.total_q && head < P.Hq, err, 0x4502)) continue;
+      const RowOut out = row_out(P, P.few, part.out, part.slot, token, head, row, FEW_ROWS);
+      store8<BF16>(out, c8, y);
+      if (c8 == 0 && out.lse != nullptr) {
+        const float lse2 = L != 0.0f ? M - BIAS + log2f(L) : -INFINITY;
+        *out.lse = part.out == OUT_FINAL ? lse2 * LN2 : lse2;
+      }
+    }
+    __syncthreads();   // the ring is free for the next part
+  }
+}
+
+template <bool BF16>
+cudaError_t launch(const SeqProb& p, WsHeader* hdr, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(few_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, RING);
+  if (e != cudaSuccess) return e;
+  few_kernel<BF16><<<p.few.grid, THREADS, RING, st>>>(p, hdr);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_few_attention(const SeqProb& p, WsHeader* hdr, cudaStream_t st) {
+  return p.bf16 ? launch<true>(p, hdr, st) : launch<false>(p, hdr, st);
+}
+
+}  // namespace ra

@@ -52,7 +52,7 @@
 #include <cuda_fp16.h>
 #include <cstdint>
 
-#include "ra_serve.h"
+#include "ra_seq.cuh"
 
 namespace ra {
 namespace {
@@ -61,9 +61,8 @@ constexpr int NUM_THREADS = 384;
 constexpr int STAGES = 2;
 constexpr int LAUNCH_REGS = 168, SOFTMAX_REGS = 208, ISSUE_REGS = 88;
 static_assert(256 * SOFTMAX_REGS + 128 * ISSUE_REGS <= NUM_THREADS * LAUNCH_REGS, "register split");
-constexpr float LN2 = 0.6931471805599453f;
-constexpr float RAISE = 8.0f;    // follow the row maximum when it rises by more than this (log2)
-constexpr int NO_TILE = 0x7fffffff;
+constexpr int SEGS = 8;           // segments in flight
+constexpr int SEG_READERS = 11;   // 8 softmax warps, 2 issuers, the copier
 
 struct Smem {
   static constexpr uint32_t QA = 0, QB = 32768;   // 32 KB each: two 16 KB swizzled halves of 64 channels
@@ -74,14 +73,9 @@ struct Smem {
 };
 
 enum : int {
-  B_KFULL = 0, B_KEMPTY = 2, B_VFULL = 4, B_VEMPTY = 6, B_QFULL = 8, B_QEMPTY = 9, B_SFULL = 10, B_PFULL = 12,
-  B_ODONE = 16, B_DRAIN = 18, B_TURN = 20, B_SEGFULL = 22, B_SEGEMPTY = 26, NBAR = 30
+  B_KFULL = 0, B_KEMPTY = 2, B_VFULL = 4, B_VEMPTY = 6, B_QFULL = 8, B_QEMPTY = 10, B_SFULL = 12, B_PFULL = 14,
+  B_ODONE = 18, B_DRAIN = 20, B_TURN = 22, B_SEGFULL = 24, B_SEGEMPTY = 32, NBAR = 40
 };
-constexpr int SEGS = 4;           // segments in flight
-constexpr int SEG_READERS = 11;   // 8 softmax warps, 2 issuers, the V copier
-
-enum : int { OUT_FINAL = 0, OUT_SLOT = 1, OUT_LEAD = 2, OUT_OWN = 3 };
-
 // A segment, as the list warp publishes it.
 struct Seg {
   int stop;
@@ -94,7 +88,7 @@ struct Seg {
   int n[2];          // tiles that query tile A / B needs
   int nload;         // tiles that are copied: max(n[0], n[1])
   int ring;          // copies before this segment
-  int qidx;          // Q copies before this segment
+  int qidx[2];       // copies of Q tile A / B before this segment
   int key0;          // packed: first key row of the sequence; paged: first key of the region
   int len;           // keys in the region
   int off;           // own region: limit of token t = clamp(t + 1 + off, 0, len) where causal
@@ -107,88 +101,9 @@ struct Misc {
   int abort_flag;
   int nf_tile[SEGS];         // per segment: first tile with repaired V elements
   Seg seg[SEGS];
-  long long scan[13];
-  long long best[13];
-  long long total, first_start;
-  int first_seq;
-  int lead_row, lead_len;
+  SharePlan plan;
 };
 static_assert(sizeof(Misc) <= 2048, "misc");
-
-struct SeqInfo {
-  int q0, Lq, k0, L, len, off, row;
-};
-
-// Sequence i's place; whatever the device-side inputs do not allow is
-// reported and left out (Lq = 0 or L = 0).
-__device__ __forceinline__ SeqInfo seq_info(const SeqProb& P, int i, DeviceErr* err) {
-  SeqInfo s;
-  s.row = -1;
-  s.k0 = 0;
-  s.L = 0;
-  if (P.cu_q != nullptr) {
-    s.q0 = P.cu_q[i];
-    const int q1 = P.cu_q[i + 1];
-    s.Lq = q1 - s.q0;
-    if (s.q0 < 0 || q1 < s.q0 || q1 > P.total_q) {
-      report(err, DEVERR_BOUNDS, 0x4001);
-      s.q0 = 0;
-      s.Lq = 0;
-    }
-  } else {
-    s.q0 = i;
-    s.Lq = 1;
-  }
-  if (P.paged) {
-    const int r = P.seqs[i];
-    if (r >= 0 && r < P.max_seqs) {
-      const int L = P.lens[r];
-      if (L >= 0 && (L + P.page_size - 1) >> P.page_shift <= P.max_pages) {
-        s.row = r;
-        s.L = L;
-      } else {
-        report(err, DEVERR_BOUNDS, 0x4002);
-      }
-    } else if (r != -1) {
-      report(err, DEVERR_BOUNDS, 0x4003);
-    }
-  } else {
-    const int k0 = P.cu_k[i], k1 = P.cu_k[i + 1];
-    if (k0 < 0 || k1 < k0 || k1 > P.total_k) {
-      report(err, DEVERR_BOUNDS, 0x4004);
-    } else {
-      s.k0 = k0;
-      s.L = k1 - k0;
-    }
-  }
-  s.len = s.L > P.shared ? s.L - P.shared : 0;
-  s.off = s.L - s.Lq - P.shared;
-  return s;
-}
-
-__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
-__device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
-
-// Key tiles of a sequence's own region per item, at least one so that rows
-// without keys are written too.
-__device__ __forceinline__ int own_tiles(const SeqInfo& s) { return max(1, (s.len + KEYS - 1) / KEYS); }
-__device__ __forceinline__ int pairs_of(const SeqProb& P, const SeqInfo& s) { return ceil_div(s.Lq, 2 * P.TQ); }
-
-// The sequence that token t belongs to: the largest i with cu_q[i] <= t.
-__device__ __forceinline__ int seq_of_token(const SeqProb& P, int t) {
-  if (P.cu_q == nullptr) return t;
-  int lo = 0, hi = P.n_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (P.cu_q[mid] <= t) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-
-__device__ __forceinline__ long long lead_tiles(const SeqProb& P) { return (P.shared + KEYS - 1) / KEYS; }
-__device__ __forceinline__ long long lead_total(const SeqProb& P) {
-  return lead_tiles(P) * P.Hkv * ceil_div(P.total_q, 2 * P.TQ);
-}
 
 // ---------------------------------------------------------------- PTX
 __device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
@@ -227,44 +142,38 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (BF16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
+// Bounded wait of a converged warp; short, since the kernel's instructions
+// have to stay in the cache.  Polls, then lets the hardware suspend the
+// threads between polls; gives up when the limit has passed or another role
+// has given up.
+struct Waits {
+  uint64_t* bar;
+  volatile int* abort_flag;
+  uint64_t limit_ns;
+  DeviceErr* err;
+};
+__device__ __noinline__ void gave_up(volatile int* abort_flag, DeviceErr* err, uint32_t site) {
+  if (!*abort_flag) report(err, DEVERR_TIMEOUT, site);
+  *abort_flag = 1;
+}
+__device__ __forceinline__ bool wait_warp(const Waits& w, int b, uint32_t parity, uint32_t site) {
+  uint64_t* bar = &w.bar[b];
+  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    const bool done = i < 32 ? mbar_test_wait(bar, parity) : mbar_try_wait_sleep(bar, parity, kSleepHintNs);
+    if (__all_sync(0xffffffffu, done)) return true;
+    if (i >= 32 && __any_sync(0xffffffffu, *w.abort_flag || globaltimer_ns() - t0 > w.limit_ns)) break;
   }
-}
-// Exponent field of a 16-bit value all ones: infinity or NaN.
-template <bool BF16>
-__device__ __forceinline__ bool nonfinite16(uint32_t h) {
-  constexpr uint32_t E = BF16 ? 0x7F80u : 0x7C00u;
-  return (h & E) == E;
-}
-template <bool BF16>
-__device__ __forceinline__ float widen16(uint32_t h) {
-  if constexpr (BF16) return __uint_as_float(h << 16);
-  return __half2float(__ushort_as_half((unsigned short)h));
-}
-
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
+  gave_up(w.abort_flag, w.err, site);
+  return false;
 }
 
 // ---------------------------------------------------------------- segment list
 // The list warp's walk; every lane holds the same values.
-struct Walk {
-  long long at, end;     // split: tiles of this CTA's share still to come; whole: first item of the next round
-  int seq;               // split: sequence that `at` lies in; whole: round
-  long long start;       // split: its first tile
-};
-
-__device__ __forceinline__ void fill_counts(const SeqProb& P, Seg& g, int tile0, int ntile) {
-  g.tile0 = tile0;
+__device__ __forceinline__ void fill_counts(const SeqProb& P, Seg& g, int t0, int t1) {
+  g.tile0 = t0;
 #pragma unroll
   for (int X = 0; X < 2; ++X) {
     const int nt = clampi(g.ntok - X * P.TQ, 0, P.TQ);
@@ -272,172 +181,112 @@ __device__ __forceinline__ void fill_counts(const SeqProb& P, Seg& g, int tile0,
     if (nt > 0) {
       const int last = g.tok + X * P.TQ + nt - 1;
       const int lim = (g.lead || !P.causal) ? g.len : clampi(last + 1 + g.off, 0, g.len);
-      n = clampi((lim + KEYS - 1) / KEYS - tile0, 0, ntile);
+      n = clampi((lim + KEYS - 1) / KEYS - t0, 0, t1 - t0);
     }
     g.n[X] = n;
   }
   g.nload = max(g.n[0], g.n[1]);
 }
 
-// The next segment of this CTA, or g.stop.
-__device__ __forceinline__ void next_segment(const SeqProb& P, const Misc* mi, Walk& w, Seg& g, DeviceErr* err) {
+// Whole items: one per CTA in rounds, every other round backwards, since
+// items get shorter along the list and this evens out what each CTA gets.
+struct Rounds {
+  long long at;
+  int round;
+};
+__device__ __forceinline__ void next_item(const SeqProb& P, Rounds& w, Seg& g, DeviceErr* err) {
+  const int per = 2 * P.TQ;
   g.stop = 0;
-  if (!P.split) {
-    const int per = 2 * P.TQ;
-    while (w.at < P.items) {
-      // rounds of one item per CTA, every other one backwards: items get
-      // shorter along the list, and this evens out what each CTA gets
-      const long long item = w.at + (w.seq & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      w.at += gridDim.x;
-      ++w.seq;
-      if (item >= P.items) continue;
-      const long long pr = P.items / P.Hkv - 1 - item / P.Hkv;
-      g.kvh = (int)(item % P.Hkv);
-      // sequence i's pairs lie at cu_q[i] / per + i and on (never more than
-      // the gap to the next sequence's first)
-      int lo = 0, hi = P.n_seqs - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (P.cu_q[mid] / per + mid <= pr) lo = mid; else hi = mid - 1;
-      }
-      const SeqInfo s = seq_info(P, lo, err);
-      const long long u = pr - (s.q0 / per + lo);
-      if (u < 0 || u >= pairs_of(P, s)) continue;
-      g.lead = 0;
-      g.row = s.row;
-      g.q0 = s.q0;
-      g.tok = (int)u * per;
-      g.ntok = min(per, s.Lq - g.tok);
-      g.key0 = P.paged ? P.shared : s.k0;
-      g.len = s.len;
-      g.off = s.off;
-      g.out = OUT_FINAL;
-      g.slot = 0;
-      fill_counts(P, g, 0, 1 << 30);
-      return;
+  while (w.at < P.items) {
+    const long long item = w.at + (w.round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    w.at += gridDim.x;
+    ++w.round;
+    if (item >= P.items) continue;
+    const int pr = (int)(P.items / P.Hkv - 1 - item / P.Hkv);
+    g.kvh = (int)(item % P.Hkv);
+    // sequence i's pairs lie at cu_q[i] / per + i and on (never more than
+    // the gap to the next sequence's first)
+    int lo = 0, hi = P.n_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (P.cu_q[mid] / per + mid <= pr) lo = mid; else hi = mid - 1;
     }
-    g.stop = 1;
-    return;
-  }
-  const long long lead_all = lead_total(P);
-  while (w.at < w.end) {
-    long long a;         // the item's first tile
-    int T;
-    if (w.at < lead_all) {
-      T = (int)lead_tiles(P);
-      const long long item = w.at / T;
-      const int pairs = ceil_div(P.total_q, 2 * P.TQ);
-      a = item * T;
-      g.lead = 1;
-      g.kvh = (int)(item / pairs);
-      g.row = mi->lead_row;
-      g.q0 = 0;
-      g.tok = (int)(item % pairs) * 2 * P.TQ;
-      g.ntok = min(2 * P.TQ, P.total_q - g.tok);
-      g.key0 = 0;
-      g.len = min(P.shared, mi->lead_len);
-      g.off = 0;
-    } else {
-      const SeqInfo s = seq_info(P, w.seq, err);
-      const int pairs = pairs_of(P, s);
-      T = own_tiles(s);
-      const long long total = (long long)T * pairs * P.Hkv;
-      if (w.at >= w.start + total) {
-        w.start += total;
-        if (++w.seq >= P.n_seqs) break;
-        continue;
-      }
-      const long long item = (w.at - w.start) / T;
-      a = w.start + item * T;
-      g.lead = 0;
-      g.kvh = (int)(item / pairs);
-      g.row = s.row;
-      g.q0 = s.q0;
-      g.tok = (int)(item % pairs) * 2 * P.TQ;
-      g.ntok = min(2 * P.TQ, s.Lq - g.tok);
-      g.key0 = P.paged ? P.shared : s.k0;
-      g.len = s.len;
-      g.off = s.off;
-    }
-    const int t0 = (int)(w.at - a);
-    const int t1 = (int)min((long long)T, w.end - a);
-    w.at = a + t1;
-    g.slot = 2 * blockIdx.x + (t0 > 0 ? 0 : 1);   // 0: began in an earlier CTA, 1: goes on in a later one
-    g.out = (t0 > 0 || t1 < T) ? OUT_SLOT : (P.shared == 0 ? OUT_FINAL : (g.lead ? OUT_LEAD : OUT_OWN));
-    fill_counts(P, g, t0, t1 - t0);
+    const SeqInfo s = seq_info(P, lo, err);
+    const int u = pr - (s.q0 / per + lo);
+    if (u < 0 || u >= ceil_div(s.Lq, per)) continue;
+    g.lead = 0;
+    g.row = s.row;
+    g.q0 = s.q0;
+    g.tok = u * per;
+    g.ntok = min(per, s.Lq - g.tok);
+    g.key0 = P.paged ? P.shared : s.k0;
+    g.len = s.len;
+    g.off = s.off;
+    g.out = OUT_FINAL;
+    g.slot = 0;
+    fill_counts(P, g, 0, 1 << 30);
     return;
   }
   g.stop = 1;
 }
 
-// Lays all items' tiles end to end: the totals, and the sequence in which
-// this CTA's share begins.  All threads.
-__device__ void plan_split(const SeqProb& P, Misc* mi, DeviceErr* err, long long& share, long long& total) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = ceil_div(P.n_seqs, NUM_THREADS);
-  const int i0 = min(P.n_seqs, tid * per), i1 = min(P.n_seqs, i0 + per);
-  long long sum = 0, best = -1;
-  for (int i = i0; i < i1; ++i) {
-    const SeqInfo s = seq_info(P, i, err);
-    sum += (long long)own_tiles(s) * pairs_of(P, s) * P.Hkv;
-    // the longest sequence, the first of them, gives the shared pages
-    best = max(best, ((long long)s.L << 32) | (uint32_t)(0x7fffffff - i));
-  }
-  long long incl = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += x;
-    best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
-  }
-  if (lane == 31) mi->scan[warp] = incl;
-  if (lane == 0) mi->best[warp] = best;
-  __syncthreads();
-  if (tid == 0) {
-    long long run = 0;
-    for (int w = 0; w < NUM_THREADS / 32; ++w) {
-      const long long x = mi->scan[w];
-      mi->scan[w] = run;
-      run += x;
-      best = max(best, mi->best[w]);
-    }
-    mi->total = run;
-    const int i = 0x7fffffff - (int)(uint32_t)(best & 0xffffffffll);
-    const SeqInfo s = seq_info(P, i, err);
-    mi->lead_row = s.row;
-    mi->lead_len = s.L;
-    mi->first_seq = 0;
-    mi->first_start = lead_total(P);
-  }
-  __syncthreads();
-  const long long lead = lead_total(P);
-  total = lead + mi->total;
-  share = (total + gridDim.x - 1) / gridDim.x;
-  const long long mine = share * blockIdx.x;
-  long long at = lead + mi->scan[warp] + incl - sum;
-  if (blockIdx.x == 0 || (mine >= at && mine < at + sum)) {
-    for (int i = i0; i < i1; ++i) {
-      const SeqInfo s = seq_info(P, i, nullptr);
-      const long long n = (long long)own_tiles(s) * pairs_of(P, s) * P.Hkv;
-      if (blockIdx.x == 0) P.starts[i] = at;
-      if (mine >= at && mine < at + n) {
-        mi->first_seq = i;
-        mi->first_start = at;
-      }
-      at += n;
-    }
-    if (blockIdx.x == 0 && i1 == P.n_seqs && i0 < i1) P.starts[P.n_seqs] = at;
-  }
-  __syncthreads();
+// Split keys: the next part of this CTA's share.
+__device__ __forceinline__ void next_part(const SeqProb& P, const SharePlan& plan, ShareWalk& w, Seg& g, DeviceErr* err) {
+  SharePart p;
+  g.stop = !next_share_part<KIND_MANY>(P, w, p, err);
+  if (g.stop) return;
+  g.lead = p.lead;
+  g.kvh = p.kvh;
+  g.tok = p.item * 2 * P.TQ;
+  g.ntok = min(2 * P.TQ, p.tokens - g.tok);
+  g.row = p.lead ? plan.lead_row : w.s.row;
+  g.q0 = p.lead ? 0 : w.s.q0;
+  g.key0 = p.lead ? 0 : P.paged ? P.shared : w.s.k0;
+  g.len = p.lead ? min(P.shared, plan.lead_len) : w.s.len;
+  g.off = p.lead ? 0 : w.s.off;
+  g.slot = p.slot;
+  g.out = p.out;
+  fill_counts(P, g, p.t0, p.t1);
 }
 
-// Address of V element (key, channel 0) of a segment's region.
-__device__ __forceinline__ const uint8_t* v_row(const SeqProb& P, const Seg& g, int key) {
-  if (!P.paged) return P.v + (long long)(g.key0 + key) * P.v_tok + g.kvh * P.v_head;
-  const int k = g.key0 + key;
-  const int page = P.table[(long long)g.row * P.max_pages + (k >> P.page_shift)];
-  if ((uint32_t)page >= (uint32_t)P.n_pages) return nullptr;
-  return P.v + page * P.v_page + (k & (P.page_size - 1)) * P.v_tok + g.kvh * P.v_head;
+// V row `row` of a tile, which holds key `key` of the region: cleared past the
+// region's end; where some row of the queries does not see it (key >= seen_by_all),
+// its non-finite elements are replaced by zero and the tile is noted.
+template <bool BF16>
+__device__ __forceinline__ void repair_v_row(uint8_t* vt, int row, int key, int len, int seen_by_all, int* nf, int tile) {
+  if (key < seen_by_all) return;
+  // 16-byte pieces, rows starting at different ones: no bank conflicts
+  auto piece = [&](int c) { return reinterpret_cast<uint4*>(vt + (c >> 3) * 16384 + row * 128) + ((c + row) & 7); };
+  if (key >= len) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) *piece(c) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+#pragma unroll 1
+  for (int c0 = 0; c0 < 16; c0 += 8) {
+    uint4 w[8];
+    bool bad = false;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) w[c] = *piece(c0 + c);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) bad |= nonfinite16<BF16>(x[e]) || nonfinite16<BF16>(x[e] >> 16);
+    }
+    if (!bad) continue;
+    atomicMin(nf, tile);
+    __threadfence_block();
+    for (int c = 0; c < 8; ++c) {
+      uint4 v = *piece(c0 + c);
+      uint32_t* x = reinterpret_cast<uint32_t*>(&v);
+      for (int e = 0; e < 4; ++e) {
+        if (nonfinite16<BF16>(x[e])) x[e] &= 0xffff0000u;
+        if (nonfinite16<BF16>(x[e] >> 16)) x[e] &= 0xffffu;
+      }
+      *piece(c0 + c) = v;
+    }
+  }
 }
 
 template <bool BF16>
@@ -471,13 +320,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(&bar[B_ODONE + i], 1);
       mbar_init(&bar[B_DRAIN + i], 1);
       mbar_init(&bar[B_TURN + i], 1);
+      mbar_init(&bar[B_QFULL + i], 1);
+      mbar_init(&bar[B_QEMPTY + i], 1);
     }
     for (int i = 0; i < SEGS; ++i) {
       mbar_init(&bar[B_SEGFULL + i], 1);
       mbar_init(&bar[B_SEGEMPTY + i], SEG_READERS);
     }
-    mbar_init(&bar[B_QFULL], 1);
-    mbar_init(&bar[B_QEMPTY], 2);
     mi->abort_flag = 0;
     fence_mbar_init();
   }
@@ -485,8 +334,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc(&mi->tmem, 512);
     tmem_relinquish();
   }
-  long long share = 0, total = 0;
-  if (P.split) plan_split(P, mi, err, share, total);
+  if (P.split) plan_shares<KIND_MANY, NUM_THREADS>(P, mi->plan, err);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -496,12 +344,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else {
     regs_dec<ISSUE_REGS>();
   }
-  auto wait = [&](int b, uint32_t parity, uint32_t site) {
-    return mbar_wait_abortable(&bar[b], parity, abort_flag, limit_ns, err, site);
-  };
-  auto wait_all = [&](int b, uint32_t parity, uint32_t site) {
-    return __all_sync(0xffffffffu, wait(b, parity, site)) != 0;
-  };
+  const Waits waits{bar, abort_flag, limit_ns, err};
+  auto wait_all = [&](int b, uint32_t parity, uint32_t site) { return wait_warp(waits, b, parity, site); };
+
   // Segment k, once it is published; a reader warp frees its place when it no
   // longer reads it.
   auto segment = [&](int k, uint32_t site) -> const Seg* {
@@ -518,7 +363,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tS = tbase + X * 128 + lane_off, tO = tbase + 256 + X * 128 + lane_off;
     const float cs = P.cs;
-    const int rtok = r / P.G, rhead = r % P.G;
+    const int rtok = over_G(P, r), rhead = r - rtok * P.G;
     uint32_t s_phase = 0, o_phase = 0;
     for (int k = 0;; ++k) {
       const Seg* seg = segment(k, 0x4101);
@@ -535,17 +380,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int t0 = g.tok + X * P.TQ, t1 = min(t0 + P.TQ, g.tok + g.ntok);
       int lim, gmin;
       if (g.lead) {
-        auto limit_of = [&](int t) {
-          const SeqInfo s = seq_info(P, seq_of_token(P, t), nullptr);
-          return clampi(t - s.q0 + 1 + s.L - s.Lq, 0, g.len);
-        };
-        lim = valid ? limit_of(tt) : 0;
+        lim = valid ? row_limit(P, g.lead, g.off, g.len, tt) : 0;
         gmin = g.len;
-        for (int t = t0 + lane; t < t1; t += 32) gmin = min(gmin, limit_of(t));
+        for (int t = t0 + lane; t < t1; t += 32) gmin = min(gmin, row_limit(P, g.lead, g.off, g.len, t));
         gmin = __reduce_min_sync(0xffffffffu, gmin);
       } else {
-        lim = P.causal ? clampi(tt + 1 + g.off, 0, g.len) : g.len;
-        gmin = P.causal ? clampi(t0 + 1 + g.off, 0, g.len) : g.len;
+        lim = row_limit(P, g.lead, g.off, g.len, tt);
+        gmin = row_limit(P, g.lead, g.off, g.len, t0);
       }
       const bool active = __any_sync(0xffffffffu, valid);
       float m = -INFINITY, l = 0.0f;
@@ -561,34 +402,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!(ok = wait_all(B_VFULL + ring % STAGES, (ring / STAGES) & 1, 0x4103))) break;
           uint8_t* vt = sm + Smem::V + (ring % STAGES) * 32768;
           const int vr = 32 * wq + lane;
-          uint4* h0 = reinterpret_cast<uint4*>(vt + vr * 128);
-          uint4* h1 = reinterpret_cast<uint4*>(vt + 16384 + vr * 128);
-          if (key + vr >= g.len) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              h0[(c + lane) & 7] = make_uint4(0, 0, 0, 0);
-              h1[(c + lane) & 7] = make_uint4(0, 0, 0, 0);
-            }
-          } else {
-            for (int c = 0; c < 16; ++c) {
-              uint4* at = (c < 8 ? h0 : h1) + ((c + lane) & 7);
-              uint4 w = *at;
-              uint32_t* x = reinterpret_cast<uint32_t*>(&w);
-              bool bad = false;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) bad |= nonfinite16<BF16>(x[e] & 0xffffu) || nonfinite16<BF16>(x[e] >> 16);
-              if (bad) {
-                atomicMin(&mi->nf_tile[k % SEGS], g.tile0 + t);
-                __threadfence_block();
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if (nonfinite16<BF16>(x[e] & 0xffffu)) x[e] &= 0xffff0000u;
-                  if (nonfinite16<BF16>(x[e] >> 16)) x[e] &= 0xffffu;
-                }
-                *at = w;
-              }
-            }
-          }
+          repair_v_row<BF16>(vt, vr, key + vr, g.len, gmin, &mi->nf_tile[k % SEGS], g.tile0 + t);
           fence_async_smem();
           __syncwarp();
         }
@@ -679,19 +493,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const float lse2 = l != 0.0f ? m - BIAS + log2f(l) : -INFINITY;
       const int token = g.q0 + tt, head = g.kvh * P.G + rhead;
       const bool store = valid && in_bounds(token >= 0 && token < P.total_q && head < P.Hq, err, 0x4105);
-      const long long grow = (long long)token * P.Hq + head;
       const int nf = *reinterpret_cast<volatile int*>(&mi->nf_tile[k % SEGS]);
-      float* frow = nullptr;
-      uint8_t* hrow = nullptr;
-      if (g.out == OUT_FINAL) {
-        hrow = P.o + token * P.o_tok + head * P.o_head;
-        if (store && P.lse != nullptr) P.lse[grow] = lse2 * LN2;
-      } else {
-        const long long at = g.out == OUT_SLOT ? (long long)g.slot * SLOT_ROWS + X * 128 + r : grow;
-        frow = (g.out == OUT_SLOT ? P.slot_o : g.out == OUT_LEAD ? P.lead_o : P.own_o) + at * D;
-        float* lrow = (g.out == OUT_SLOT ? P.slot_lse : g.out == OUT_LEAD ? P.lead_lse : P.own_lse) + at;
-        if (store) *lrow = lse2;
-      }
+      const RowOut out = row_out(P, P.many, g.out, g.slot, store ? token : 0, store ? head : 0, X * 128 + r);
+      if (store && out.lse != nullptr) *out.lse = g.out == OUT_FINAL ? lse2 * LN2 : lse2;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         float y[32];
@@ -706,135 +510,128 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int e = 0; e < 32; ++e) y[e] = 0.0f;
         }
         if (nf != NO_TILE && store) {
-          // non-finite elements of V that were taken out of the product, for
-          // the rows that see them
-          const int last = min(lim, (g.tile0 + n) * KEYS);
-          for (int key = nf * KEYS; key < last; ++key) {
-            const uint8_t* vp = v_row(P, g, key);
-            if (vp == nullptr) continue;
-            const uint32_t* x = reinterpret_cast<const uint32_t*>(vp + 64 * c);
+          float z[32];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const uint32_t w = x[e];
-              if (nonfinite16<BF16>(w & 0xffffu)) y[2 * e] += widen16<BF16>(w & 0xffffu);
-              if (nonfinite16<BF16>(w >> 16)) y[2 * e + 1] += widen16<BF16>(w >> 16);
-            }
-          }
+          for (int e = 0; e < 32; ++e) z[e] = y[e];
+          add_nonfinite<BF16, 32>(P, {g.key0, g.row, g.kvh}, nf * KEYS, min(lim, (g.tile0 + n) * KEYS), 32 * c, z);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = z[e];
         }
         if (store) {
-          if (hrow != nullptr) {
-            uint4* dst = reinterpret_cast<uint4*>(hrow + 64 * c);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              dst[q] = make_uint4(pack2<BF16>(y[8 * q], y[8 * q + 1]), pack2<BF16>(y[8 * q + 2], y[8 * q + 3]),
-                                  pack2<BF16>(y[8 * q + 4], y[8 * q + 5]), pack2<BF16>(y[8 * q + 6], y[8 * q + 7]));
-          } else {
-            float4* dst = reinterpret_cast<float4*>(frow + 32 * c);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) dst[q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
-          }
+          for (int q = 0; q < 4; ++q) store8<BF16>(out, 32 * c + 8 * q, y + 8 * q);
         }
       }
       tc_fence_before();   // O has been read: the next segment's first P.V follows this row's next P
       free_segment(k);
     }
-  } else if (warp == 8 || warp == 11) {
-    // ------------------------------------------------------------ copies
-    const bool isK = warp == 8;
-    const int FULL = isK ? B_KFULL : B_VFULL, EMPTY = isK ? B_KEMPTY : B_VEMPTY;
-    const uint32_t base = isK ? Smem::K : Smem::V;
-    const CUtensorMap* map = isK ? &mk : &mv;
-    if (lane == 0) {
-      asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-      if (isK) asm volatile("prefetch.tensormap [%0];" ::"l"(&mq) : "memory");
-    }
-    Walk w;
-    if (P.split) {
-      w.at = share * blockIdx.x;
-      w.end = min(total, w.at + share);
-      w.seq = mi->first_seq;
-      w.start = mi->first_start;
-    } else {
-      w.at = w.end = w.start = 0;
-      w.seq = 0;
-    }
-    int ring = 0, qidx = 0;
-    bool ok = true;
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ segment list
+    Rounds rounds{0, 0};
+    ShareWalk w;
+    if (P.split) start_walk<KIND_MANY>(P, mi->plan, w);
+    int ring = 0, q0 = 0, q1 = 0;
     Seg g;
+    for (int k = 0;; ++k) {
+      if (P.split) next_part(P, mi->plan, w, g, err);
+      else next_item(P, rounds, g, err);
+      g.ring = ring;
+      g.qidx[0] = q0;
+      g.qidx[1] = q1;
+      if (k >= SEGS && !wait_all(B_SEGEMPTY + k % SEGS, (k / SEGS - 1) & 1, 0x4201)) break;
+      if (lane == 0) {
+        mi->seg[k % SEGS] = g;
+        mi->nf_tile[k % SEGS] = NO_TILE;
+        __threadfence_block();
+        mbar_arrive(&bar[B_SEGFULL + k % SEGS]);
+      }
+      __syncwarp();
+      if (g.stop) break;
+      ring += g.nload;
+      q0 += g.n[0] > 0;
+      q1 += g.n[1] > 0;
+    }
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ copies
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&mq) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&mk) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&mv) : "memory");
+    }
+    // lane = (K or V, half of the channels, page of the tile)
+    const int box_half = (lane >> 3) & 1, box_page = lane & 7;
+    const CUtensorMap* map = lane < 16 ? &mk : &mv;
+    uint8_t* const base = sm + (lane < 16 ? Smem::K : Smem::V) + box_half * 16384;
+    const int full = lane < 16 ? B_KFULL : B_VFULL;
+    int ring = 0, qn[2] = {0, 0};
+    bool ok = true;
     for (int k = 0; ok; ++k) {
-      if (isK) {
-        next_segment(P, mi, w, g, err);
-        g.ring = ring;
-        g.qidx = qidx;
-        if (k >= SEGS && !(ok = wait_all(B_SEGEMPTY + k % SEGS, (k / SEGS - 1) & 1, 0x4201))) break;
+      const Seg* seg = segment(k, 0x4203);
+      if (!(ok = seg != nullptr) || seg->stop) break;
+      const Seg& g = *seg;
+      const int nload = g.nload, len = g.len, key0 = g.key0, kvh = g.kvh;
+#pragma unroll
+      for (int X = 0; X < 2; ++X) {
+        if (!ok || (X ? g.n[1] : g.n[0]) == 0) continue;
+        const int c = qn[X];
+        if (c > 0 && !(ok = wait_all(B_QEMPTY + X, (c - 1) & 1, 0x4202))) continue;
         if (lane == 0) {
-          mi->seg[k % SEGS] = g;
-          mi->nf_tile[k % SEGS] = NO_TILE;
-          __threadfence_block();
-          mbar_arrive(&bar[B_SEGFULL + k % SEGS]);
+          mbar_expect_tx(&bar[B_QFULL + X], 2u * 128u * P.G * P.TQ);
+          for (int h = 0; h < 2; ++h)
+            tma_load4(sm + (X ? Smem::QB : Smem::QA) + h * 16384, &mq, 64 * h, 0, kvh, g.q0 + g.tok + X * P.TQ,
+                      &bar[B_QFULL + X]);
         }
         __syncwarp();
-        if (g.stop) break;
-        if (g.nload > 0) {
-          if (qidx > 0 && !(ok = wait_all(B_QEMPTY, (qidx - 1) & 1, 0x4202))) break;
-          if (lane == 0) {
-            const int nq = g.n[1] > 0 ? 2 : 1;
-            mbar_expect_tx(&bar[B_QFULL], nq * 2u * 128u * P.G * P.TQ);
-            for (int X = 0; X < nq; ++X)
-              for (int h = 0; h < 2; ++h)
-                tma_load4(sm + (X ? Smem::QB : Smem::QA) + h * 16384, &mq, 64 * h, 0, g.kvh,
-                          g.q0 + g.tok + X * P.TQ, &bar[B_QFULL]);
-          }
-          __syncwarp();
-          ++qidx;
-        }
-      } else {
-        const Seg* seg = segment(k, 0x4203);
-        if (!(ok = seg != nullptr)) break;
-        g = *seg;
-        free_segment(k);
-        if (g.stop) break;
+        ++qn[X];
       }
-      for (int t = 0; t < g.nload; ++t, ++ring) {
+      if (!ok) break;
+      const int* trow = P.paged ? P.table + (long long)g.row * P.max_pages : nullptr;
+      // this lane's page of tile t; -1: none
+      auto page_of = [&](int t) {
+        const int first = (g.tile0 + t) * KEYS + (box_page << P.page_shift);
+        if (t >= nload || box_page >= KEYS >> P.page_shift || first >= len) return -1;
+        const int page = trow[(key0 + first) >> P.page_shift];
+        if ((uint32_t)page < (uint32_t)P.n_pages) return page;
+        report(err, DEVERR_BOUNDS, 0x4204);   // not a page: read as zeros
+        return P.n_pages;
+      };
+      int page = P.paged ? page_of(0) : -1;
+      for (int t = 0; t < nload; ++t, ++ring) {
         const int st = ring % STAGES;
-        const int key = (g.tile0 + t) * KEYS;
-        int page = 0;
-        bool box = false;
-        if (P.paged) {
-          // lane b copies the page that holds the tile's keys b * page_size and on
-          const int first = key + (lane << P.page_shift);
-          box = lane < (KEYS >> P.page_shift) && first < g.len;
-          if (box) {
-            page = P.table[(long long)g.row * P.max_pages + ((g.key0 + first) >> P.page_shift)];
-            if ((uint32_t)page >= (uint32_t)P.n_pages) {   // not a page: read as zeros
-              report(err, DEVERR_BOUNDS, 0x4204);
-              page = P.n_pages;
-            }
+        const uint32_t parity = ((ring / STAGES) - 1) & 1;
+        const int next = P.paged ? page_of(t + 1) : -1;
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));   // four per page
+        if (ring >= STAGES && !(ok = wait_all(B_KEMPTY + st, parity, 0x4205))) break;
+        const uint32_t bytes = P.paged ? boxes * 64u * P.page_size : 32768u;
+        if (lane == 0) mbar_expect_tx(&bar[B_KFULL + st], bytes);
+        __syncwarp();
+        auto issue = [&] {
+          if (P.paged) {
+            if (page >= 0)
+              tma_load4(base + st * 32768 + ((box_page << P.page_shift) * 128), map, 64 * box_half, 0, kvh, page,
+                        &bar[full + st]);
+          } else if (box_page == 0) {
+            tma_load4(base + st * 32768, map, 64 * box_half, 0, kvh, key0 + (g.tile0 + t) * KEYS, &bar[full + st]);
           }
-        }
-        if (ring >= STAGES && !(ok = wait_all(EMPTY + st, ((ring / STAGES) - 1) & 1, 0x4205))) break;
-        uint8_t* dst = sm + base + st * 32768;
-        if (P.paged) {
-          const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
-          if (lane == 0) mbar_expect_tx(&bar[FULL + st], boxes * 256u * P.page_size);
-          __syncwarp();
-          if (box) {
-            uint8_t* d = dst + ((lane << P.page_shift) * 128);
-            tma_load4(d, map, 0, 0, g.kvh, page, &bar[FULL + st]);
-            tma_load4(d + 16384, map, 64, 0, g.kvh, page, &bar[FULL + st]);
-          }
-          __syncwarp();
-        } else if (lane == 0) {
-          mbar_expect_tx(&bar[FULL + st], 32768u);
-          tma_load4(dst, map, 0, 0, g.kvh, g.key0 + key, &bar[FULL + st]);
-          tma_load4(dst + 16384, map, 64, 0, g.kvh, g.key0 + key, &bar[FULL + st]);
-        }
+        };
+        if (lane < 16) issue();
+        __syncwarp();
+        if (ring >= STAGES && !(ok = wait_all(B_VEMPTY + st, parity, 0x4206))) break;
+        if (lane == 0) mbar_expect_tx(&bar[B_VFULL + st], bytes);
+        __syncwarp();
+        if (lane >= 16) issue();
+        __syncwarp();
+        page = next;
       }
+      free_segment(k);
     }
     // every copy lands before the CTA exits, also after another role gave up
-    if (isK && qidx > 0) mbar_wait(&bar[B_QFULL], (qidx - 1) & 1, limit_ns, err, 0x4206);
-    for (int t = ring > STAGES ? ring - STAGES : 0; t < ring; ++t)
-      mbar_wait(&bar[FULL + t % STAGES], (t / STAGES) & 1, limit_ns, err, 0x4207);
+    for (int X = 0; X < 2; ++X)
+      if (qn[X] > 0) mbar_wait(&bar[B_QFULL + X], (qn[X] - 1) & 1, limit_ns, err, 0x4207);
+    for (int t = ring > STAGES ? ring - STAGES : 0; t < ring; ++t) {
+      mbar_wait(&bar[B_KFULL + t % STAGES], (t / STAGES) & 1, limit_ns, err, 0x4208);
+      mbar_wait(&bar[B_VFULL + t % STAGES], (t / STAGES) & 1, limit_ns, err, 0x4209);
+    }
   } else {
     // ------------------------------------------------------------ MMA issuers
     // One warp per query tile.  They take turns, tile A's P.V(t) and S(t+1),
@@ -849,15 +646,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint64_t qd = kmajor_desc(smem_u32(sm + Smem::QA)) + X * (32768 >> 4);
     const uint64_t kd = kmajor_desc(smem_u32(sm + Smem::K)), vd = nmajor_desc(smem_u32(sm + Smem::V));
     const uint32_t tS = __shfl_sync(0xffffffffu, tbase, 0) + X * 128, tO = tS + 256;
-    uint32_t p_phase = 0;
+    uint32_t p_phase[2] = {0, 0};
     int turn = 0;                  // groups of this tile so far
-    auto spin_all = [&](int b, uint32_t parity, uint32_t site) {
-      // polls without suspending at first, then as every other wait
-#pragma unroll 1
-      for (int i = 0; i < 64; ++i)
-        if (__all_sync(0xffffffffu, mbar_test_wait(&bar[b], parity))) return true;
-      return wait_all(b, parity, site);
-    };
     auto issue_S = [&](int ring) {   // S = Q K^T
       const uint64_t kt = kd + (ring % STAGES) * (32768 >> 4);
       if (elect_one()) {
@@ -875,7 +665,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const Seg& g = *seg;
       const int nload = __shfl_sync(0xffffffffu, g.nload, 0), ring0 = __shfl_sync(0xffffffffu, g.ring, 0);
       const int n = __shfl_sync(0xffffffffu, X ? g.n[1] : g.n[0], 0);
-      const int q_phase = __shfl_sync(0xffffffffu, g.qidx & 1, 0), stop = __shfl_sync(0xffffffffu, g.stop, 0);
+      const int q = __shfl_sync(0xffffffffu, X ? g.qidx[1] : g.qidx[0], 0);
+      const int stop = __shfl_sync(0xffffffffu, g.stop, 0);
       free_segment(k);
       if (stop) break;
       if (nload == 0) continue;
@@ -886,14 +677,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (elect_one()) {
           if (mma) umma_commit(&bar[B_KEMPTY + (ring0 + t) % STAGES]);
           else mbar_arrive(&bar[B_KEMPTY + (ring0 + t) % STAGES]);
-          if (t == nload - 1) {
-            if (mma) umma_commit(&bar[B_QEMPTY]);
-            else mbar_arrive(&bar[B_QEMPTY]);
-          }
+          if (t == n - 1) umma_commit(&bar[B_QEMPTY + X]);
         }
         __syncwarp();
       };
-      if (!(ok = wait_all(B_QFULL, q_phase, 0x4304) && k_full(0))) break;
+      if (n > 0 && !(ok = wait_all(B_QFULL + X, q & 1, 0x4304))) break;
+      if (!(ok = k_full(0))) break;
       tc_fence_after();
       if (n > 0) issue_S(ring0);
       k_done(0, n > 0);
@@ -904,13 +693,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (t + 1 < nload && !(ok = k_full(t + 1))) break;
         // A goes first; its first turn needs no leave
         if (X == 1 || turn > 0) {
-          if (!(ok = spin_all(B_TURN + X, (X ? turn : turn - 1) & 1, 0x4306))) break;
+          if (!(ok = wait_all(B_TURN + X, (X ? turn : turn - 1) & 1, 0x4306))) break;
         }
         ++turn;
         if (t < n) {
 #pragma unroll
           for (int half = 0; half < 2; ++half) {   // O += P(t) V(t), P from TMEM
-            if (!ok || !(ok = spin_all(B_PFULL + 2 * half + X, p_phase, 0x4305))) continue;
+            if (!ok || !(ok = wait_all(B_PFULL + 2 * half + X, p_phase[half], 0x4305))) continue;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -920,7 +709,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             __syncwarp();
           }
           if (!ok) break;
-          p_phase ^= 1u;
+          p_phase[0] ^= 1u;
+          p_phase[1] ^= 1u;
           if (t + 1 < n) {
             issue_S(ring + 1);
           } else {
@@ -952,70 +742,84 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
 // Joins partial rows: one warp per (token, head), four channels per lane.
 //   o = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M),  M = max lse_s
-// over the parts the split kernel left: the shared region's and the own
-// region's, each whole or in slots of consecutive CTAs.  Memory-bound: reads
-// 516 bytes per part and row, writes 256.
+// over the parts of the shared region and of the own region, each whole or in
+// slots of consecutive CTAs.  Memory-bound: reads 516 bytes per part and row,
+// writes 256.
+struct Parts {
+  const float *o, *l;   // part c: o + (first + c step) 128, l + first + c step
+  long long first, step;
+  int n;
+};
+template <int KIND>
+__device__ __forceinline__ Parts parts_of(const SeqProb& P, const ShareBuf& b, bool lead, const SeqInfo& s, int i, int token,
+                                          int head, long long row) {
+  using K = Kind<KIND>;
+  const Items it = items_of<KIND>(P, lead ? P.total_q : s.Lq, lead ? P.shared : s.len);
+  const int t = lead ? token : token - s.q0, per = K::tokens_per_item(P), u = t / per, tt = t % per;
+  const int kvh = head / P.G, gh = head - kvh * P.G;
+  const long long total = b.starts[P.n_seqs], share = share_of(total, b.grid);
+  const long long a = (lead ? 0 : b.starts[i]) + (kvh * it.count + u) * it.units<KIND>() + K::W_ITEM;
+  const int c0 = share_at(a, share), c1 = share_at(a + (long long)(it.T - 1) * K::W_TILE, share);
+  Parts p;
+  if (c0 == c1) {
+    p.o = lead ? P.lead_o : P.own_o;
+    p.l = lead ? P.lead_lse : P.own_lse;
+    p.first = row;
+    p.step = 0;
+    p.n = 1;
+  } else {   // the item goes on behind CTA c0's share (slot 1), began before the others' (slot 0)
+    p.o = b.slot_o;
+    p.l = b.slot_lse;
+    p.first = 2ll * c0 * K::SLOT + slot_row<KIND>(P, tt, gh);
+    p.step = 2ll * K::SLOT;
+    p.n = c1 - c0 + 1;
+  }
+  return p;
+}
 template <bool BF16>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ SeqProb P) {
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= (long long)P.total_q * P.Hq) return;
-  const int token = (int)(row / P.Hq), head = (int)(row % P.Hq);
-  const int kvh = head / P.G, gh = head % P.G, per = 2 * P.TQ;
+  const int token = (int)((uint32_t)row / (uint32_t)P.Hq), head = (int)((uint32_t)row % (uint32_t)P.Hq);
   const int i = seq_of_token(P, token);
   const SeqInfo s = seq_info(P, i, nullptr);
   if (token < s.q0 || token >= s.q0 + s.Lq) return;   // behind the last sequence
-  const long long total = P.starts[P.n_seqs];
-  const long long share = (total + P.grid - 1) / P.grid;
-  long long a[2];        // first tile of the two regions' items
-  int T[2], in[2];       // tiles; the row's index within its slot
-  const int r0 = P.shared > 0 ? 0 : 1;
-  {
-    const int pairs = ceil_div(P.total_q, per), u = token / per, tt = token % per;
-    T[0] = (int)lead_tiles(P);
-    a[0] = (long long)(kvh * pairs + u) * T[0];
-    in[0] = (tt / P.TQ) * 128 + (tt % P.TQ) * P.G + gh;
+  Parts parts[2];
+  parts[1] = takes<KIND_FEW>(P, s.Lq) ? parts_of<KIND_FEW>(P, P.few, false, s, i, token, head, row)
+                                      : parts_of<KIND_MANY>(P, P.many, false, s, i, token, head, row);
+  if (P.shared > 0) {
+    parts[0] = takes<KIND_FEW>(P, P.total_q) ? parts_of<KIND_FEW>(P, P.few, true, s, i, token, head, row)
+                                             : parts_of<KIND_MANY>(P, P.many, true, s, i, token, head, row);
+  } else {
+    parts[0].n = 0;
+    if (parts[1].n == 1) return;   // final already
   }
-  {
-    const int t = token - s.q0, u = t / per, tt = t % per;
-    T[1] = own_tiles(s);
-    a[1] = P.starts[i] + (long long)(kvh * pairs_of(P, s) + u) * T[1];
-    in[1] = (tt / P.TQ) * 128 + (tt % P.TQ) * P.G + gh;
-  }
-  if (r0 == 1 && a[1] / share == (a[1] + T[1] - 1) / share) return;   // final already
+  // part c of the first CTA lies one slot further than `first` says
+  auto at = [&](const Parts& p, int c) { return p.first + c * p.step + (p.n > 1 && c == 0 ? p.step / 2 : 0); };
   float M = -INFINITY;
 #pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    if (g < r0) continue;
-    const float* whole_l = g ? P.own_lse : P.lead_lse;
-    const long long c0 = a[g] / share, c1 = (a[g] + T[g] - 1) / share;
-    if (c0 == c1) {
-      M = fmaxf(M, whole_l[row]);
-    } else {
-      for (long long c = c0; c <= c1; ++c) M = fmaxf(M, P.slot_lse[(2 * c + (c == c0)) * SLOT_ROWS + in[g]]);
-    }
-  }
+  for (int g = 0; g < 2; ++g)
+    for (int c = lane; c < parts[g].n; c += 32) M = fmaxf(M, parts[g].l[at(parts[g], c)]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
   float sum = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (M != -INFINITY) {
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      if (g < r0) continue;
-      const float *whole_o = g ? P.own_o : P.lead_o, *whole_l = g ? P.own_lse : P.lead_lse;
-      const long long c0 = a[g] / share, c1 = (a[g] + T[g] - 1) / share;
-      for (long long c = c0; c <= c1; ++c) {
-        const long long at = c0 == c1 ? row : (2 * c + (c == c0)) * SLOT_ROWS + in[g];
-        const float l = c0 == c1 ? whole_l[at] : P.slot_lse[at];
-        if (l == -INFINITY) continue;                  // saw no key
-        const float w = exp2f(l - M);
-        const float4 x = reinterpret_cast<const float4*>((c0 == c1 ? whole_o : P.slot_o) + at * D)[lane];
+    for (int g = 0; g < 2; ++g)
+#pragma unroll 4
+      for (int c = 0; c < parts[g].n; ++c) {
+        const long long k = at(parts[g], c);
+        const float l = parts[g].l[k];
+        const float4 x = reinterpret_cast<const float4*>(parts[g].o + k * D)[lane];
+        const float w = l == -INFINITY ? 0.0f : exp2f(l - M);   // 0: saw no key, all zeros
         sum += w;
         acc.x = fmaf(w, x.x, acc.x);
         acc.y = fmaf(w, x.y, acc.y);
         acc.z = fmaf(w, x.z, acc.z);
         acc.w = fmaf(w, x.w, acc.w);
       }
-    }
   }
   const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
   const uint2 out = make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
@@ -1024,19 +828,23 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Se
 }
 
 template <bool BF16>
-cudaError_t launch(const SeqProb& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, void* ws,
+cudaError_t launch(const SeqProb& p, const SeqMaps& m, void* ws,
                    cudaStream_t st) {
-  const int smem = Smem::BYTES + 1024;   // > half the SM: one CTA per SM owns all 512 TMEM columns
-  auto kern = seq_attn_kernel<BF16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa;   // the setmaxnreg split needs exactly LAUNCH_REGS at launch
-  e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs != LAUNCH_REGS) return cudaErrorInvalidConfiguration;
-  kern<<<p.grid, NUM_THREADS, smem, st>>>(p, mq, mk, mv, static_cast<WsHeader*>(ws), wait_limit());
-  e = cudaGetLastError();
-  if (e != cudaSuccess || !p.split) return e;
+  cudaError_t e;
+  if (p.few.grid > 0 && (e = launch_few_attention(p, static_cast<WsHeader*>(ws), st)) != cudaSuccess) return e;
+  if (p.many.grid > 0) {
+    const int smem = Smem::BYTES + 1024;   // > half the SM: one CTA per SM owns all 512 TMEM columns
+    auto kern = seq_attn_kernel<BF16>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;   // the setmaxnreg split needs exactly LAUNCH_REGS at launch
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != LAUNCH_REGS) return cudaErrorInvalidConfiguration;
+    kern<<<p.many.grid, NUM_THREADS, smem, st>>>(p, m.q, m.k, m.v, static_cast<WsHeader*>(ws), wait_limit());
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (!p.split) return cudaSuccess;
   const long long rows = (long long)p.total_q * p.Hq;
   combine_kernel<BF16><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p);
   return cudaGetLastError();
@@ -1044,9 +852,8 @@ cudaError_t launch(const SeqProb& p, const CUtensorMap& mq, const CUtensorMap& m
 
 }  // namespace
 
-cudaError_t launch_seq_attention(const SeqProb& p, const CUtensorMap& mq, const CUtensorMap& mk,
-                                 const CUtensorMap& mv, void* ws, cudaStream_t st) {
-  return p.bf16 ? launch<true>(p, mq, mk, mv, ws, st) : launch<false>(p, mq, mk, mv, ws, st);
+cudaError_t launch_seq_attention(const SeqProb& p, const SeqMaps& m, void* ws, cudaStream_t st) {
+  return p.bf16 ? launch<true>(p, m, ws, st) : launch<false>(p, m, ws, st);
 }
 
 }  // namespace ra

@@ -107,7 +107,9 @@ ra_status sm_count(int* out) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
   return e == cudaSuccess ? RA_OK : cuda_fail(e, "device query");
 }
-constexpr int SM_BOUND = 148;   // workspace sizes are fixed without a device: at most this many CTAs split keys
+
+// Workspace sizes are fixed without a device: at most this many SMs work on split keys.
+constexpr int SM_BOUND = 148;
 
 // ---------------------------------------------------------------- packed
 ra_status check_packed(const ra_packed* p) {
@@ -201,6 +203,7 @@ ra_status check_attn(const ra_cache_problem* p, const ra_cache_attn* a) {
   if (a->total_q < 0) return fail(RA_ERR_INVALID_ARG, "negative token count");
   if (a->total_q > (1 << 30) || a->n_seqs > (1 << 24))
     return fail(RA_ERR_UNSUPPORTED, "at most 2^30 tokens and 2^24 sequences");
+  if ((long long)a->total_q * a->Hq >= (1ll << 31)) return fail(RA_ERR_UNSUPPORTED, "2^31 query rows or more");
   if (a->layer < 0 || a->layer >= p->layers) return fail(RA_ERR_INVALID_ARG, "layer %d of %d", a->layer, p->layers);
   if (a->shared < 0 || a->shared % p->page_size != 0)
     return fail(RA_ERR_INVALID_ARG, "shared = %d is not a multiple of the page size %d", a->shared, p->page_size);
@@ -217,30 +220,43 @@ void fill_common(ra::SeqProb* P, int n_seqs, int Hq, int Hkv, int total_q, int d
   P->Hq = Hq;
   P->Hkv = Hkv;
   P->G = Hq / Hkv;
+  P->inv_G = (65536 + P->G - 1) / P->G;
   P->TQ = 128 / P->G;
   P->total_q = total_q;
   P->bf16 = dtype == RA_BF16;
   P->cs = log2_scale(scale);
 }
 
-bool q_map(CUtensorMap* m, const ra::SeqProb& P, const void* q, long long tok, long long head) {
+bool q_map(ra::SeqMaps* m, const ra::SeqProb& P, const void* q, long long tok, long long head) {
   const cuuint64_t outer[3] = {(cuuint64_t)P.G, (cuuint64_t)P.Hkv, (cuuint64_t)P.total_q};
   const cuuint64_t h = map_stride(head, P.Hq);
   const cuuint64_t stride[3] = {h, h * P.G, map_stride(tok, P.total_q)};
   const cuuint32_t box[3] = {(cuuint32_t)P.G, 1, (cuuint32_t)P.TQ};
-  return make_map(m, P.bf16, q, outer, stride, box);
+  return make_map(&m->q, P.bf16, q, outer, stride, box);
 }
 
-void bind_ws(ra::SeqProb* P, void* ws) {
-  const ra::SeqWs L = ra::seq_ws(P->n_seqs, P->total_q, P->Hq, P->shared, P->grid);
+void bind_ws(ra::SeqProb* P, int many, int few, void* ws) {
+  const ra::SeqWs L = ra::seq_ws(P->n_seqs, P->total_q, P->Hq, P->shared, many, few);
   char* b = static_cast<char*>(ws);
-  P->starts = reinterpret_cast<long long*>(b + L.starts);
-  P->slot_o = reinterpret_cast<float*>(b + L.slot_o);
-  P->slot_lse = reinterpret_cast<float*>(b + L.slot_lse);
-  P->lead_o = reinterpret_cast<float*>(b + L.lead_o);
-  P->lead_lse = reinterpret_cast<float*>(b + L.lead_lse);
-  P->own_o = reinterpret_cast<float*>(b + L.own_o);
-  P->own_lse = reinterpret_cast<float*>(b + L.own_lse);
+  auto floats = [&](size_t o) { return reinterpret_cast<float*>(b + o); };
+  P->many.starts = reinterpret_cast<long long*>(b + L.many_starts);
+  P->many.slot_o = floats(L.many_o);
+  P->many.slot_lse = floats(L.many_lse);
+  P->few.starts = reinterpret_cast<long long*>(b + L.few_starts);
+  P->few.slot_o = floats(L.few_o);
+  P->few.slot_lse = floats(L.few_lse);
+  P->lead_o = floats(L.lead_o);
+  P->lead_lse = floats(L.lead_lse);
+  P->own_o = floats(L.own_o);
+  P->own_lse = floats(L.own_lse);
+}
+
+// Which kernels a cache call may need: sequences of unknown query lengths may
+// go to either.
+void cache_kinds(const ra_cache_attn* a, int G, bool single, bool* many, bool* few) {
+  const bool lead_few = (long long)a->total_q * G <= ra::FEW_ROWS, one_few = G <= ra::FEW_ROWS;
+  *few = one_few;
+  *many = (a->shared > 0 && !lead_few) || (single ? !one_few : !lead_few);
 }
 
 }  // namespace
@@ -250,7 +266,7 @@ extern "C" {
 size_t ra_packed_workspace_bytes(const ra_packed* p) {
   if (check_packed(p) != RA_OK) return 0;
   if (!packed_split(p)) return align256(sizeof(ra::WsHeader));
-  return ra::seq_ws(p->n_seqs, p->total_q, p->Hq, 0, SM_BOUND).total;
+  return ra::seq_ws(p->n_seqs, p->total_q, p->Hq, 0, SM_BOUND, 0).total;
 }
 
 ra_status ra_packed_attention_fwd(const ra_packed* p, const void* q, const void* k, const void* v, const int* cu_q,
@@ -285,10 +301,10 @@ ra_status ra_packed_attention_fwd(const ra_packed* p, const void* q, const void*
   P.split = packed_split(p);
   int sms = 0;
   if ((st = sm_count(&sms)) != RA_OK) return st;
-  P.grid = sms < SM_BOUND ? sms : SM_BOUND;
-  if (!P.split && P.items < P.grid) P.grid = (int)P.items;
-  if (P.split) bind_ws(&P, ws);
-  CUtensorMap mq, mk, mv;
+  P.many.grid = sms < SM_BOUND ? sms : SM_BOUND;
+  if (!P.split && P.items < P.many.grid) P.many.grid = (int)P.items;
+  if (P.split) bind_ws(&P, SM_BOUND, 0, ws);
+  ra::SeqMaps m;
   const void* kb = p->total_k > 0 ? k : q;   // no keys at all: no copy of them is issued
   const void* vb = p->total_k > 0 ? v : q;
   const cuuint64_t rows = p->total_k > 0 ? p->total_k : 1;
@@ -296,10 +312,10 @@ ra_status ra_packed_attention_fwd(const ra_packed* p, const void* q, const void*
   const cuuint64_t ks[3] = {256, map_stride(p->k_head, p->Hkv), map_stride(p->k_token, p->total_k)};
   const cuuint64_t vs[3] = {256, map_stride(p->v_head, p->Hkv), map_stride(p->v_token, p->total_k)};
   const cuuint32_t box[3] = {1, 1, ra::KEYS};
-  if (!q_map(&mq, P, q, p->q_token, p->q_head) || !make_map(&mk, P.bf16, kb, outer, ks, box) ||
-      !make_map(&mv, P.bf16, vb, outer, vs, box))
+  if (!q_map(&m, P, q, p->q_token, p->q_head) || !make_map(&m.k, P.bf16, kb, outer, ks, box) ||
+      !make_map(&m.v, P.bf16, vb, outer, vs, box))
     return fail(RA_ERR_CUDA, "tensor map of q, k or v");
-  const cudaError_t e = ra::launch_seq_attention(P, mq, mk, mv, ws, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = ra::launch_seq_attention(P, m, ws, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RA_OK : cuda_fail(e, "packed attention launch");
 }
 
@@ -417,7 +433,9 @@ ra_status ra_cache_compact(const ra_cache_problem* p, const ra_cache* c, void* w
 
 size_t ra_cache_attention_workspace_bytes(const ra_cache_problem* p, const ra_cache_attn* a) {
   if (check_attn(p, a) != RA_OK) return 0;
-  return ra::seq_ws(a->n_seqs, a->total_q, a->Hq, a->shared, SM_BOUND).total;
+  bool many, few;   // with cu_q, which needs the most
+  cache_kinds(a, a->Hq / p->Hkv, false, &many, &few);
+  return ra::seq_ws(a->n_seqs, a->total_q, a->Hq, a->shared, many ? SM_BOUND : 0, few ? ra::FEW_CTAS * SM_BOUND : 0).total;
 }
 
 ra_status ra_cache_attention_fwd(const ra_cache_problem* p, const ra_cache* c, const ra_cache_attn* a, const void* q,
@@ -456,6 +474,10 @@ ra_status ra_cache_attention_fwd(const ra_cache_problem* p, const ra_cache* c, c
   const size_t layer = (size_t)256 * p->n_pages * p->Hkv * p->page_size;
   const uint8_t* kb = static_cast<const uint8_t*>(c->k) + a->layer * layer;
   const uint8_t* vb = static_cast<const uint8_t*>(c->v) + a->layer * layer;
+  P.q = static_cast<const uint8_t*>(q);
+  P.q_tok = 2 * a->q_token;
+  P.q_head = 2 * a->q_head;
+  P.k = kb;
   P.v = vb;
   P.v_tok = 256;
   P.v_head = 256ll * p->page_size;
@@ -467,16 +489,21 @@ ra_status ra_cache_attention_fwd(const ra_cache_problem* p, const ra_cache* c, c
   P.split = 1;
   int sms = 0;
   if ((st = sm_count(&sms)) != RA_OK) return st;
-  P.grid = sms < SM_BOUND ? sms : SM_BOUND;
-  bind_ws(&P, ws);
-  CUtensorMap mq, mk, mv;
+  if (sms > SM_BOUND) sms = SM_BOUND;
+  bool many, few;
+  cache_kinds(a, P.G, false, &many, &few);
+  bind_ws(&P, many ? SM_BOUND : 0, few ? ra::FEW_CTAS * SM_BOUND : 0, ws);
+  cache_kinds(a, P.G, cu_q == nullptr, &many, &few);
+  P.many.grid = many ? sms : 0;
+  P.few.grid = few ? ra::FEW_CTAS * sms : 0;
+  ra::SeqMaps m;
   const cuuint64_t outer[3] = {(cuuint64_t)p->page_size, (cuuint64_t)p->Hkv, (cuuint64_t)p->n_pages};
   const cuuint64_t stride[3] = {256, (cuuint64_t)P.v_head, (cuuint64_t)P.v_page};
   const cuuint32_t box[3] = {(cuuint32_t)p->page_size, 1, 1};
-  if (!q_map(&mq, P, q, a->q_token, a->q_head) || !make_map(&mk, P.bf16, kb, outer, stride, box) ||
-      !make_map(&mv, P.bf16, vb, outer, stride, box))
+  if (!q_map(&m, P, q, a->q_token, a->q_head) || !make_map(&m.k, P.bf16, kb, outer, stride, box) ||
+      !make_map(&m.v, P.bf16, vb, outer, stride, box))
     return fail(RA_ERR_CUDA, "tensor map of q or the pool");
-  const cudaError_t e = ra::launch_seq_attention(P, mq, mk, mv, ws, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = ra::launch_seq_attention(P, m, ws, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RA_OK : cuda_fail(e, "cache attention launch");
 }
 
