@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(THREADS, FEW_CTAS) few_kernel(const __grid_con
   __shared__ int nf_tile;                           // first tile with values taken out of V
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   DeviceErr* err = &hdr->err;
+  dependents_may_start();
   plan_shares<KIND_FEW, THREADS>(P, plan, err);
   ShareWalk w;
   start_walk<KIND_FEW>(P, plan, w);
@@ -110,8 +111,6 @@ __global__ void __launch_bounds__(THREADS, FEW_CTAS) few_kernel(const __grid_con
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if (tid == 0) nf_tile = NO_TILE;
-    copy_tile(part.t0, 0);
-    copy_tile(n > 1 ? part.t0 + 1 : NO_COPY, 1);   // past the part's end: nothing, but a group all the same
     // this warp's 16 rows of Q as operand registers; rows past the last are zero
     uint32_t q[8][4];
     int lim[2], gmin = len;
@@ -140,9 +139,11 @@ __global__ void __launch_bounds__(THREADS, FEW_CTAS) few_kernel(const __grid_con
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[c][e] = 0.0f;
 
+    // tiles are copied two ahead; the body stands once, for the instruction cache
 #pragma unroll 1
-    for (int t = 0; t < n; ++t) {
+    for (int t = -2; t < n; ++t) {
       const int key = (part.t0 + t) * FEW_KEYS, stage = t & 1;
+      if (t >= 0) {
       wait_copies<1>();
       __syncthreads();
       const uint32_t kt = ring + stage * 2 * HALF_STAGE, vt = kt + HALF_STAGE;
@@ -228,6 +229,7 @@ __global__ void __launch_bounds__(THREADS, FEW_CTAS) few_kernel(const __grid_con
         }
       }
       __syncthreads();   // the stage has been read
+      }
       copy_tile(t + 2 < n ? part.t0 + t + 2 : NO_COPY, stage);
     }
     wait_copies<0>();
@@ -253,15 +255,35 @@ __global__ void __launch_bounds__(THREADS, FEW_CTAS) few_kernel(const __grid_con
     }
     __syncthreads();
     const int nf = nf_tile;
-    for (int idx = tid; idx < rows * 16; idx += THREADS) {
-      const int row = idx >> 4, c8 = (idx & 15) * 8, b = row >> 4, r = row & 15;
-      float M = -INFINITY;
+    // a row's factors, once: 2^(m - M) / L of each group
+    if (tid < rows) {
+      const int b = tid >> 4, r = tid & 15;
+      float M = -INFINITY, L = 0.0f;
       for (int g = 0; g < groups; ++g) M = max3_nan(M, stat_m[g * blocks + b][r], M);
-      float L = 0.0f, y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       for (int g = 0; g < groups; ++g) {
         const int v = g * blocks + b;
         const float f = stat_m[v][r] == -INFINITY ? 0.0f : ex2(stat_m[v][r] - M);
         L = fmaf(f, stat_l[v][r], L);
+        stat_m[v][r] = f;
+      }
+      const float inv = L != 0.0f ? 1.0f / L : 0.0f;   // a row without keys: zeros
+      for (int g = 0; g < groups; ++g) stat_m[g * blocks + b][r] *= inv;
+      const int t = over_G(P, tid), token = q0 + t, head = part.kvh * P.G + tid - t * P.G;
+      const RowOut out = row_out(P, P.few, part.out, part.slot, token, head, tid, FEW_ROWS);
+      const float lse2 = L != 0.0f ? M - BIAS + log2f(L) : -INFINITY;
+      if (out.lse != nullptr && in_bounds(token < P.total_q && head < P.Hq, err, 0x4503))
+        *out.lse = part.out == OUT_FINAL ? lse2 * LN2 : lse2;
+    }
+    __syncthreads();
+#pragma unroll 2
+    for (int row = tid >> 4; row < rows; row += 8) {
+      const int c8 = (tid & 15) * 8, b = row >> 4, r = row & 15;
+      float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (g >= groups) continue;
+        const int v = g * blocks + b;
+        const float f = stat_m[v][r];
         const float4* x = reinterpret_cast<const float4*>(join + (v * 16 + r) * D);
         const float4 x0 = x[(c8 / 4) ^ (r & 7)], x1 = x[(c8 / 4 + 1) ^ (r & 7)];
         y[0] = fmaf(f, x0.x, y[0]);
@@ -273,20 +295,18 @@ __global__ void __launch_bounds__(THREADS, FEW_CTAS) few_kernel(const __grid_con
         y[6] = fmaf(f, x1.z, y[6]);
         y[7] = fmaf(f, x1.w, y[7]);
       }
-      const float inv = 1.0f / L;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = L != 0.0f ? y[e] * inv : 0.0f;   // a row without keys; NaN stays
       const int t = over_G(P, row), token = q0 + t, head = part.kvh * P.G + row - t * P.G;
-      if (nf != NO_TILE)
+      if (nf != NO_TILE) {
+        float z[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = y[e];
         add_nonfinite<BF16, 8>(P, {key0, table_row, part.kvh}, nf * FEW_KEYS,
-                               min(row_limit(P, part.lead, off, len, t), part.t1 * FEW_KEYS), c8, y);
-      if (!in_bounds(token < P.total_q && head < P.Hq, err, 0x4502)) continue;
-      const RowOut out = row_out(P, P.few, part.out, part.slot, token, head, row, FEW_ROWS);
-      store8<BF16>(out, c8, y);
-      if (c8 == 0 && out.lse != nullptr) {
-        const float lse2 = L != 0.0f ? M - BIAS + log2f(L) : -INFINITY;
-        *out.lse = part.out == OUT_FINAL ? lse2 * LN2 : lse2;
+                               min(row_limit(P, part.lead, off, len, t), part.t1 * FEW_KEYS), c8, z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = z[e];
       }
+      if (in_bounds(token < P.total_q && head < P.Hq, err, 0x4502))
+        store8<BF16>(row_out(P, P.few, part.out, part.slot, token, head, row, FEW_ROWS), c8, y);
     }
     __syncthreads();   // the ring is free for the next part
   }

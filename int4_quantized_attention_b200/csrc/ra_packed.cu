@@ -306,6 +306,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   DeviceErr* err = &hdr->err;
 
+  dependents_may_start();
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&bar[B_KFULL + i], 1);
@@ -732,6 +733,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncwarp();
     mbar_wait(&bar[B_DRAIN + X], 0, limit_ns, err, 0x4306);
   }
+  // the kernel of few rows may still run: this grid ends after it, so that the
+  // joining kernel, which waits for this one, finds both results
+  wait_for_predecessor();
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
@@ -759,7 +763,7 @@ __device__ __forceinline__ Parts parts_of(const SeqProb& P, const ShareBuf& b, b
   const int kvh = head / P.G, gh = head - kvh * P.G;
   const long long total = b.starts[P.n_seqs], share = share_of(total, b.grid);
   const long long a = (lead ? 0 : b.starts[i]) + (kvh * it.count + u) * it.units<KIND>() + K::W_ITEM;
-  const int c0 = share_at(a, share), c1 = share_at(a + (long long)(it.T - 1) * K::W_TILE, share);
+  const int c0 = quotient(a, share), c1 = quotient(a + (long long)(it.T - 1) * K::W_TILE, share);
   Parts p;
   if (c0 == c1) {
     p.o = lead ? P.lead_o : P.own_o;
@@ -778,6 +782,7 @@ __device__ __forceinline__ Parts parts_of(const SeqProb& P, const ShareBuf& b, b
 }
 template <bool BF16>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ SeqProb P) {
+  wait_for_predecessor();
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= (long long)P.total_q * P.Hq) return;
@@ -831,7 +836,11 @@ template <bool BF16>
 cudaError_t launch(const SeqProb& p, const SeqMaps& m, void* ws,
                    cudaStream_t st) {
   cudaError_t e;
-  if (p.few.grid > 0 && (e = launch_few_attention(p, static_cast<WsHeader*>(ws), st)) != cudaSuccess) return e;
+  bool first = true;
+  if (p.few.grid > 0) {
+    if ((e = launch_few_attention(p, static_cast<WsHeader*>(ws), st)) != cudaSuccess) return e;
+    first = false;
+  }
   if (p.many.grid > 0) {
     const int smem = Smem::BYTES + 1024;   // > half the SM: one CTA per SM owns all 512 TMEM columns
     auto kern = seq_attn_kernel<BF16>;
@@ -841,13 +850,13 @@ cudaError_t launch(const SeqProb& p, const SeqMaps& m, void* ws,
     e = cudaFuncGetAttributes(&fa, kern);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != LAUNCH_REGS) return cudaErrorInvalidConfiguration;
-    kern<<<p.many.grid, NUM_THREADS, smem, st>>>(p, m.q, m.k, m.v, static_cast<WsHeader*>(ws), wait_limit());
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_after(!first, kern, p.many.grid, NUM_THREADS, smem, st, p, m.q, m.k, m.v, static_cast<WsHeader*>(ws),
+                     wait_limit());
+    if (e != cudaSuccess) return e;
   }
   if (!p.split) return cudaSuccess;
   const long long rows = (long long)p.total_q * p.Hq;
-  combine_kernel<BF16><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_after(true, combine_kernel<BF16>, (unsigned)((rows + 7) / 8), 256, 0, st, p);
 }
 
 }  // namespace

@@ -83,6 +83,28 @@ __device__ __forceinline__ int seq_of_token(const SeqProb& P, int t) {
   return lo;
 }
 
+// ---------------------------------------------------------------- launches
+// The kernels of one call follow each other without waiting for the last CTA
+// of the one before to leave (programmatic dependent launch): the next grid's
+// CTAs take the SMs that become free, prepare, and wait here for the results.
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <class... Params, class... Args>
+cudaError_t launch_after(bool overlap, void (*kern)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+                         Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // ---------------------------------------------------------------- shares
 // The two kernels a call may use.  KIND_MANY: 128-row query tiles on the
 // tensor-memory MMA, items of two tiles.  KIND_FEW: at most FEW_ROWS rows over
@@ -99,7 +121,7 @@ struct Kind<KIND_MANY> {
 };
 template <>
 struct Kind<KIND_FEW> {
-  static constexpr int TILE_KEYS = FEW_KEYS, W_ITEM = 3, W_TILE = 2, SLOT = FEW_ROWS;
+  static constexpr int TILE_KEYS = FEW_KEYS, W_ITEM = 5, W_TILE = 2, SLOT = FEW_ROWS;
   __device__ static __forceinline__ int tokens_per_item(const SeqProb& P) { return FEW_ROWS; }
 };
 
@@ -138,15 +160,16 @@ __device__ __forceinline__ long long units_of(const SeqProb& P, int tokens, int 
   return i.units<KIND>() * i.count * P.Hkv;
 }
 
+// a / b for a quotient that fits an int; mostly 32-bit.
+__device__ __forceinline__ int quotient(long long a, long long b) {
+  return (a | b) >> 32 == 0 ? (int)((uint32_t)a / (uint32_t)b) : (int)(a / b);
+}
+
 // A CTA's share of all units: at least an item of one tile, so that every CTA
 // between an item's first and last holds one of its tiles.
 __device__ __forceinline__ long long share_of(long long total, int ctas) {
-  return max((total + ctas - 1) / ctas, 6ll);
-}
-
-// Which CTA's share unit a lies in.
-__device__ __forceinline__ int share_at(long long a, long long share) {
-  return (a | share) >> 32 == 0 ? (int)((uint32_t)a / (uint32_t)share) : (int)(a / share);
+  const long long t = total + ctas - 1;
+  return max(t >> 32 == 0 ? (long long)((uint32_t)t / (uint32_t)ctas) : t / ctas, 7ll);
 }
 
 // In shared memory: the plan of one CTA.
@@ -256,7 +279,7 @@ __device__ __forceinline__ void start_walk(const SeqProb& P, const SharePlan& pl
   }
   if (w.seq < 0 && P.shared == 0) w.seq = 0;
   know<KIND>(P, w, nullptr);
-  w.item = (int)((w.at - w.start) / w.it.units<KIND>());
+  w.item = quotient(w.at - w.start, w.it.units<KIND>());
   w.start += w.item * w.it.units<KIND>();
 }
 // The next part of the share; false at its end.
