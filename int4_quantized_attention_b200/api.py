@@ -407,19 +407,22 @@ def _dtype(call: str, dtype) -> int:
 
 def _rows(call: str, name: str, t, dtype, device, heads=None, tokens=None):
     """Checks a [tokens, heads, 128] tensor whose last dimension is contiguous."""
-    if t.dim() != 3 or t.dtype != dtype or t.device != device or t.shape[2] != 128 or \
-            (t.stride(2) != 1 and t.numel()) or (heads is not None and t.shape[1] != heads) or \
-            (tokens is not None and t.shape[0] != tokens):
-        raise _bad(call, f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}; want "
-                         f"[{'tokens' if tokens is None else tokens}, {'heads' if heads is None else heads}, 128] "
-                         f"{dtype} on {device} with a contiguous last dimension")
+    shape = t.shape
+    if len(shape) == 3 and shape[2] == 128 and t.dtype == dtype and t.device == device and \
+            (t.stride(2) == 1 or not t.numel()) and (heads is None or shape[1] == heads) and \
+            (tokens is None or shape[0] == tokens):
+        return
+    raise _bad(call, f"{name}: {tuple(shape)} {t.dtype} on {t.device}, strides {t.stride()}; want "
+                     f"[{'tokens' if tokens is None else tokens}, {'heads' if heads is None else heads}, 128] "
+                     f"{dtype} on {device} with a contiguous last dimension")
 
 
 def _ints(call: str, name: str, t, device, n=None):
     import torch
-    if t.dim() != 1 or t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or \
-            (n is not None and t.numel() != n):
-        raise _bad(call, f"{name}: a contiguous 1-D int32 tensor{'' if n is None else f' of {n}'} on {device}")
+    if t.dtype == torch.int32 and t.device == device and t.dim() == 1 and t.is_contiguous() and \
+            (n is None or t.numel() == n):
+        return
+    raise _bad(call, f"{name}: a contiguous 1-D int32 tensor{'' if n is None else f' of {n}'} on {device}")
 
 
 class _Workspace:
@@ -429,16 +432,17 @@ class _Workspace:
     def __init__(self, device):
         self.device, self.buffers = device, []
 
-    def get(self, need: int):
+    def current(self):
+        return self.buffers[-1] if self.buffers else self.grow(256)
+
+    def grow(self, need: int):
         import torch
-        if not self.buffers or self.buffers[-1].numel() < need:
-            size = need if not self.buffers else max(need, 2 * self.buffers[-1].numel())
-            self.buffers.append(torch.zeros((size,), dtype=torch.uint8, device=self.device))
+        size = max(need, 2 * self.buffers[-1].numel()) if self.buffers else need
+        self.buffers.append(torch.zeros((size,), dtype=torch.uint8, device=self.device))
         return self.buffers[-1]
 
     def check(self):
-        import torch
-        with torch.cuda.device(self.device):
+        with _on(self.device):
             for b in self.buffers:
                 check_device_error(b)
 
@@ -476,9 +480,17 @@ class PackedAttention:
         p = Packed(cu_q.numel() - 1, Hq, k.shape[1], 128, code, int(bool(causal)), total_q, k.shape[0], scale,
                    q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
                    out.stride(0), out.stride(1))
-        need = packed_workspace_bytes(p)
-        with _on(self.device):
-            packed_attention_fwd(p, q, k, v, cu_q, cu_k, out, lse, self._ws.get(need or 256))
+        ref = ctypes.byref(p)
+        with _on(self.device) as stream:
+            for last in (False, True):
+                ws = self._ws.current()
+                status = lib().ra_packed_attention_fwd(
+                    ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), out.data_ptr(),
+                    None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+                if last or status != RA_ERR_WORKSPACE:
+                    break
+                self._ws.grow(packed_workspace_bytes(p))
+            _check("ra_packed_attention_fwd", status)
         return (out, lse) if lse is not None else out
 
     def check(self) -> None:
@@ -487,7 +499,8 @@ class PackedAttention:
 
 
 class _on:
-    """Makes a tensor's device the current one for a call."""
+    """Makes a tensor's device the current one for a call; gives its current stream."""
+    __slots__ = ("index", "before")
 
     def __init__(self, device):
         self.index, self.before = device.index, None
@@ -498,10 +511,11 @@ class _on:
         if now != self.index:
             self.before = now
             torch.cuda.set_device(self.index)
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
-        import torch
         if self.before is not None:
+            import torch
             torch.cuda.set_device(self.before)
 
 
@@ -548,16 +562,20 @@ class PagedCache:
         self.table = state[at(self.c.table):at(self.c.table) + max_seqs * max_pages].view(max_seqs, max_pages)
         self._work = torch.zeros((cache_workspace_bytes(self.p),), dtype=torch.uint8, device=self.device)
         self._ws = _Workspace(self.device)
+        self._rp, self._rc = ctypes.byref(self.p), ctypes.byref(self.c)
         if fresh:
             with _on(self.device):
                 cache_init(self.p, self.c)
+
+    def _call(self, name: str, *args) -> None:
+        with _on(self.device) as stream:
+            _check(name, getattr(lib(), name)(self._rp, self._rc, *args, self._work.data_ptr(), self._work.numel(), stream))
 
     def extend(self, seqs, n_new) -> None:
         """Rows `seqs` grow by `n_new` tokens (int32 device lists; -1 rows are passed over)."""
         _ints("cache_extend", "seqs", seqs, self.device)
         _ints("cache_extend", "n_new", n_new, self.device, seqs.numel())
-        with _on(self.device):
-            cache_extend(self.p, self.c, seqs, n_new, self._work)
+        self._call("ra_cache_extend", seqs.data_ptr(), n_new.data_ptr(), seqs.numel())
 
     def write(self, layer: int, seqs, k, v, cu_new=None) -> None:
         """The last tokens of rows `seqs` in one layer: k, v [tokens, Hkv, 128];
@@ -568,26 +586,24 @@ class PagedCache:
             _ints(call, "cu_new", cu_new, self.device, seqs.numel() + 1)
         _rows(call, "k", k, self.dtype, self.device, self.p.Hkv)
         _rows(call, "v", v, self.dtype, self.device, self.p.Hkv, k.shape[0])
-        with _on(self.device):
-            cache_write(self.p, self.c, layer, seqs, cu_new, k, v, self._work)
+        (kt, kh, _), (vt, vh, _) = k.stride(), v.stride()
+        self._call("ra_cache_write", layer, seqs.data_ptr(), None if cu_new is None else cu_new.data_ptr(), seqs.numel(),
+                   k.shape[0], k.data_ptr(), v.data_ptr(), kt, kh, vt, vh)
 
     def fork(self, parents, children) -> None:
         """Empty rows `children` become copies of rows `parents`, sharing their full pages."""
         _ints("cache_fork", "parents", parents, self.device)
         _ints("cache_fork", "children", children, self.device, parents.numel())
-        with _on(self.device):
-            cache_fork(self.p, self.c, parents, children, self._work)
+        self._call("ra_cache_fork", parents.data_ptr(), children.data_ptr(), children.numel())
 
     def free(self, seqs) -> None:
         """Rows `seqs` become empty."""
         _ints("cache_free", "seqs", seqs, self.device)
-        with _on(self.device):
-            cache_free(self.p, self.c, seqs, self._work)
+        self._call("ra_cache_free", seqs.data_ptr(), seqs.numel())
 
     def compact(self) -> None:
         """Moves the n live pages to the first n places."""
-        with _on(self.device):
-            cache_compact(self.p, self.c, self._work)
+        self._call("ra_cache_compact")
 
     def attention(self, layer: int, q, seqs, cu_q=None, shared: int = 0, scale: float = 0.0, out=None, lse=None,
                   return_lse: bool = False):
@@ -608,9 +624,17 @@ class PagedCache:
         lse = _lse(call, lse, return_lse, total_q, Hq, self.device)
         a = CacheAttn(seqs.numel(), Hq, total_q, layer, shared, scale, q.stride(0), q.stride(1), out.stride(0),
                       out.stride(1))
-        need = cache_attention_workspace_bytes(self.p, a)
-        with _on(self.device):
-            cache_attention_fwd(self.p, self.c, a, q, seqs, cu_q, out, lse, self._ws.get(need or 256))
+        ref = ctypes.byref(a)
+        with _on(self.device) as stream:
+            for last in (False, True):
+                ws = self._ws.current()
+                status = lib().ra_cache_attention_fwd(
+                    self._rp, self._rc, ref, q.data_ptr(), seqs.data_ptr(), None if cu_q is None else cu_q.data_ptr(),
+                    out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+                if last or status != RA_ERR_WORKSPACE:
+                    break
+                self._ws.grow(cache_attention_workspace_bytes(self.p, a))
+            _check("ra_cache_attention_fwd", status)
         return (out, lse) if lse is not None else out
 
     def check(self) -> None:

@@ -30,6 +30,7 @@ namespace {
 constexpr int CL = 8;              // CTAs of the state cluster
 constexpr int CT = 1024;           // threads per CTA of it
 constexpr int ALL = CL * CT;
+constexpr int COPY_CTAS = 8 * 148;   // 2048 threads per SM
 
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -393,11 +394,7 @@ __global__ void __launch_bounds__(256)
 }
 
 cudaError_t launch_copy(const CacheProb& c, const Ws& w, int remap, cudaStream_t st) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  copy_kernel<<<8 * sms, 256, 0, st>>>(c, w, remap);
+  copy_kernel<<<COPY_CTAS, 256, 0, st>>>(c, w, remap);
   return cudaGetLastError();
 }
 

@@ -73,12 +73,14 @@ __global__ void __launch_bounds__(THREADS, FEW_CTAS) few_kernel(const __grid_con
   DeviceErr* err = &hdr->err;
   dependents_may_start();
   plan_shares<KIND_FEW, THREADS>(P, plan, err);
-  ShareWalk w;
-  start_walk<KIND_FEW>(P, plan, w);
+  ShareWalk<KIND_FEW> w;
+  start_walk(P, plan, w);
+  SplitItem* const split = P.few.split + blockIdx.x;
+  if (tid == 0) split->parts = 0;
   const uint32_t ring = smem_u32(sm);
   const int copy_row = tid >> 4, copy_piece = tid & 15;   // this thread's rows of a tile: copy_row + 8 i
   SharePart part;
-  while (next_share_part<KIND_FEW>(P, w, part, err)) {
+  while (next_share_part(P, plan, w, part, err)) {
     const int rows = part.tokens * P.G, n = part.t1 - part.t0;
     const int blocks = rows <= 16 ? 1 : rows <= 32 ? 2 : 4, groups = 4 / blocks;
     const int block = warp & (blocks - 1), group = warp >> (blocks >> 1);
@@ -111,6 +113,7 @@ __global__ void __launch_bounds__(THREADS, FEW_CTAS) few_kernel(const __grid_con
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if (tid == 0) nf_tile = NO_TILE;
+    if (tid == 0 && part.out == OUT_SLOT && (part.slot & 1)) *split = {part.parts, q0, part.tokens, part.kvh};
     // this warp's 16 rows of Q as operand registers; rows past the last are zero
     uint32_t q[8][4];
     int lim[2], gmin = len;
@@ -314,7 +317,9 @@ __global__ void __launch_bounds__(THREADS, FEW_CTAS) few_kernel(const __grid_con
 
 template <bool BF16>
 cudaError_t launch(const SeqProb& p, WsHeader* hdr, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(few_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, RING);
+  static OncePerDevice once;
+  const cudaError_t e = once.run(
+      [] { return cudaFuncSetAttribute(few_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, RING); });
   if (e != cudaSuccess) return e;
   few_kernel<BF16><<<p.few.grid, THREADS, RING, st>>>(p, hdr);
   return cudaGetLastError();

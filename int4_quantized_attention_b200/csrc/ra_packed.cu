@@ -20,7 +20,7 @@
 //   split        all key tiles of all items, laid end to end, are cut into
 //                equal shares, one per CTA, whatever the lengths are; an item
 //                that crosses a border leaves partial rows (fp32) that
-//                combine_kernel joins.  For few rows over many keys, and
+//                the joining kernel puts together.  For few rows over many keys, and
 //                wherever there is a shared region.
 //
 // 384 threads, the pipeline of the FP16 fallback kernel:
@@ -68,7 +68,8 @@ struct Smem {
   static constexpr uint32_t QA = 0, QB = 32768;   // 32 KB each: two 16 KB swizzled halves of 64 channels
   static constexpr uint32_t K = 65536;            // STAGES x 32 KB
   static constexpr uint32_t V = 131072;           // STAGES x 32 KB
-  static constexpr uint32_t MISC = 196608;
+  static constexpr uint32_t STAGE = 196608;       // 2 KB per softmax warp: rows on their way out
+  static constexpr uint32_t MISC = STAGE + 16384;
   static constexpr uint32_t BYTES = MISC + 2048;
 };
 
@@ -231,9 +232,9 @@ __device__ __forceinline__ void next_item(const SeqProb& P, Rounds& w, Seg& g, D
 }
 
 // Split keys: the next part of this CTA's share.
-__device__ __forceinline__ void next_part(const SeqProb& P, const SharePlan& plan, ShareWalk& w, Seg& g, DeviceErr* err) {
+__device__ __forceinline__ void next_part(const SeqProb& P, const SharePlan& plan, ShareWalk<KIND_MANY>& w, Seg& g, DeviceErr* err) {
   SharePart p;
-  g.stop = !next_share_part<KIND_MANY>(P, w, p, err);
+  g.stop = !next_share_part(P, plan, w, p, err);
   if (g.stop) return;
   g.lead = p.lead;
   g.kvh = p.kvh;
@@ -246,47 +247,50 @@ __device__ __forceinline__ void next_part(const SeqProb& P, const SharePlan& pla
   g.off = p.lead ? 0 : w.s.off;
   g.slot = p.slot;
   g.out = p.out;
+  if (p.out == OUT_SLOT && (p.slot & 1)) P.many.split[blockIdx.x] = {p.parts, g.q0 + g.tok, g.ntok, g.kvh};
   fill_counts(P, g, p.t0, p.t1);
 }
 
 // V row `row` of a tile, which holds key `key` of the region: cleared past the
-// region's end; where some row of the queries does not see it (key >= seen_by_all),
-// its non-finite elements are replaced by zero and the tile is noted.
+// region's end; where some row of the queries does not see it (key >=
+// seen_by_all), its non-finite elements are replaced by zero and the tile is
+// noted.  Returns whether it wrote.
 template <bool BF16>
-__device__ __forceinline__ void repair_v_row(uint8_t* vt, int row, int key, int len, int seen_by_all, int* nf, int tile) {
-  if (key < seen_by_all) return;
+__device__ __forceinline__ bool repair_v_row(uint8_t* vt, int row, int key, int len, int seen_by_all, int* nf, int tile) {
+  if (key < seen_by_all) return false;
   // 16-byte pieces, rows starting at different ones: no bank conflicts
   auto piece = [&](int c) { return reinterpret_cast<uint4*>(vt + (c >> 3) * 16384 + row * 128) + ((c + row) & 7); };
   if (key >= len) {
 #pragma unroll
     for (int c = 0; c < 16; ++c) *piece(c) = make_uint4(0, 0, 0, 0);
-    return;
+    return true;
   }
-#pragma unroll 1
+  // an exponent of all ones, plus one, carries into the sign's place
+  constexpr uint32_t E = BF16 ? 0x7F807F80u : 0x7C007C00u, ONE = BF16 ? 0x00800080u : 0x04000400u;
+  uint32_t carry = 0;
+#pragma unroll
   for (int c0 = 0; c0 < 16; c0 += 8) {
     uint4 w[8];
-    bool bad = false;
 #pragma unroll
     for (int c = 0; c < 8; ++c) w[c] = *piece(c0 + c);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) bad |= nonfinite16<BF16>(x[e]) || nonfinite16<BF16>(x[e] >> 16);
-    }
-    if (!bad) continue;
-    atomicMin(nf, tile);
-    __threadfence_block();
-    for (int c = 0; c < 8; ++c) {
-      uint4 v = *piece(c0 + c);
-      uint32_t* x = reinterpret_cast<uint32_t*>(&v);
-      for (int e = 0; e < 4; ++e) {
-        if (nonfinite16<BF16>(x[e])) x[e] &= 0xffff0000u;
-        if (nonfinite16<BF16>(x[e] >> 16)) x[e] &= 0xffffu;
-      }
-      *piece(c0 + c) = v;
-    }
+    for (int c = 0; c < 8; ++c)
+      carry |= ((w[c].x & E) + ONE) | ((w[c].y & E) + ONE) | ((w[c].z & E) + ONE) | ((w[c].w & E) + ONE);
   }
+  if ((carry & 0x80008000u) == 0) return false;
+  atomicMin(nf, tile);
+  __threadfence_block();
+#pragma unroll 1
+  for (int c = 0; c < 16; ++c) {
+    uint4 v = *piece(c);
+    uint32_t* x = reinterpret_cast<uint32_t*>(&v);
+    for (int e = 0; e < 4; ++e) {
+      if (nonfinite16<BF16>(x[e])) x[e] &= 0xffff0000u;
+      if (nonfinite16<BF16>(x[e] >> 16)) x[e] &= 0xffffu;
+    }
+    *piece(c) = v;
+  }
+  return true;
 }
 
 template <bool BF16>
@@ -381,12 +385,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int t0 = g.tok + X * P.TQ, t1 = min(t0 + P.TQ, g.tok + g.ntok);
       int lim, gmin;
       if (g.lead) {
-        lim = valid ? row_limit(P, g.lead, g.off, g.len, tt) : 0;
+        lim = row_limit(P, 1, 0, g.len, min(tt, t1 - 1));
         gmin = g.len;
         for (int t = t0 + lane; t < t1; t += 32) gmin = min(gmin, row_limit(P, g.lead, g.off, g.len, t));
         gmin = __reduce_min_sync(0xffffffffu, gmin);
       } else {
-        lim = row_limit(P, g.lead, g.off, g.len, tt);
+        lim = row_limit(P, 0, g.off, g.len, min(tt, t1 - 1));
         gmin = row_limit(P, g.lead, g.off, g.len, t0);
       }
       const bool active = __any_sync(0xffffffffu, valid);
@@ -403,8 +407,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!(ok = wait_all(B_VFULL + ring % STAGES, (ring / STAGES) & 1, 0x4103))) break;
           uint8_t* vt = sm + Smem::V + (ring % STAGES) * 32768;
           const int vr = 32 * wq + lane;
-          repair_v_row<BF16>(vt, vr, key + vr, g.len, gmin, &mi->nf_tile[k % SEGS], g.tile0 + t);
-          fence_async_smem();
+          if (repair_v_row<BF16>(vt, vr, key + vr, g.len, gmin, &mi->nf_tile[k % SEGS], g.tile0 + t))
+            fence_async_smem();   // the products read it
           __syncwarp();
         }
         if (active) {
@@ -413,11 +417,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
           tmem_wait_ld();
-          const int nvalid = lim - key;
-          if (__any_sync(0xffffffffu, nvalid < KEYS)) {
+          const int nvalid = lim - key;   // keys of the tile that this row sees
+          if (gmin < key + KEYS) {
 #pragma unroll
-            for (int e = 0; e < 128; ++e)
-              if (e >= nvalid) s[e] = 0xFF800000u;   // -inf: out of the max and the sum
+            for (int c = 0; c < 4; ++c) {   // bit e: key 32 c + e is seen
+              const uint32_t bits = nvalid >= 32 * c + 32 ? 0xffffffffu : ~(0xffffffffu << max(0, nvalid - 32 * c));
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if ((bits >> e & 1u) == 0) s[32 * c + e] = 0xFF800000u;   // -inf: out of the max and the sum
+            }
           }
           // a NaN score makes the maximum, and so the row, NaN
           float mh[8];
@@ -497,6 +505,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int nf = *reinterpret_cast<volatile int*>(&mi->nf_tile[k % SEGS]);
       const RowOut out = row_out(P, P.many, g.out, g.slot, store ? token : 0, store ? head : 0, X * 128 + r);
       if (store && out.lse != nullptr) *out.lse = g.out == OUT_FINAL ? lse2 * LN2 : lse2;
+      // A row per lane would touch 32 lines with every store.  64 bytes of each
+      // row go through shared memory instead (pieces XORed with the row pair: no
+      // bank conflicts), and four lanes write a row: eight rows per store.
+      uint8_t* const mine = out.h != nullptr ? out.h : reinterpret_cast<uint8_t*>(out.f);
+      uint8_t* dst[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int from = 8 * i + (lane >> 2);
+        const unsigned long long p = __shfl_sync(0xffffffffu, store ? (unsigned long long)(uintptr_t)mine : 0ull, from);
+        dst[i] = reinterpret_cast<uint8_t*>((uintptr_t)p);
+      }
+      uint4* const stage = reinterpret_cast<uint4*>(sm + Smem::STAGE) + warp * 128;
+      auto put = [&](const uint32_t* words, int off) {   // 16 words of every row, to byte `off` of it
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+          stage[lane * 4 + (p ^ ((lane >> 1) & 3))] = make_uint4(words[4 * p], words[4 * p + 1], words[4 * p + 2], words[4 * p + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int from = 8 * i + (lane >> 2);
+          const uint4 v = stage[from * 4 + ((lane & 3) ^ ((from >> 1) & 3))];
+          if (dst[i] != nullptr) *reinterpret_cast<uint4*>(dst[i] + off + 16 * (lane & 3)) = v;
+        }
+        __syncwarp();
+      };
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         float y[32];
@@ -518,9 +551,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] = z[e];
         }
-        if (store) {
+        uint32_t words[32];
+        if (g.out == OUT_FINAL) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) store8<BF16>(out, 32 * c + 8 * q, y + 8 * q);
+          for (int e = 0; e < 16; ++e) words[e] = pack2<BF16>(y[2 * e], y[2 * e + 1]);
+          put(words, 64 * c);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) words[e] = __float_as_uint(y[e]);
+          put(words, 128 * c);
+          put(words + 16, 128 * c + 64);
         }
       }
       tc_fence_before();   // O has been read: the next segment's first P.V follows this row's next P
@@ -529,8 +569,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else if (warp == 8) {
     // ------------------------------------------------------------ segment list
     Rounds rounds{0, 0};
-    ShareWalk w;
-    if (P.split) start_walk<KIND_MANY>(P, mi->plan, w);
+    ShareWalk<KIND_MANY> w;
+    if (P.split) {
+      start_walk(P, mi->plan, w);
+      if (lane == 0) P.many.split[blockIdx.x].parts = 0;
+      __syncwarp();
+    }
     int ring = 0, q0 = 0, q1 = 0;
     Seg g;
     for (int k = 0;; ++k) {
@@ -744,92 +788,98 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-// Joins partial rows: one warp per (token, head), four channels per lane.
-//   o = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M),  M = max lse_s
-// over the parts of the shared region and of the own region, each whole or in
-// slots of consecutive CTAs.  Memory-bound: reads 516 bytes per part and row,
-// writes 256.
-struct Parts {
-  const float *o, *l;   // part c: o + (first + c step) 128, l + first + c step
-  long long first, step;
+// ---------------------------------------------------------------- join
+// o = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M),  M = max lse_s, over the
+// partial results of a row: one warp per row, four channels per lane.
+// Memory-bound: reads 516 bytes per part and row, writes 256.
+struct Parts {           // part c lies at first + c step (+ back for c = 0)
+  const float *o, *l;
+  long long first, step, back;
   int n;
 };
-template <int KIND>
-__device__ __forceinline__ Parts parts_of(const SeqProb& P, const ShareBuf& b, bool lead, const SeqInfo& s, int i, int token,
-                                          int head, long long row) {
-  using K = Kind<KIND>;
-  const Items it = items_of<KIND>(P, lead ? P.total_q : s.Lq, lead ? P.shared : s.len);
-  const int t = lead ? token : token - s.q0, per = K::tokens_per_item(P), u = t / per, tt = t % per;
-  const int kvh = head / P.G, gh = head - kvh * P.G;
-  const long long total = b.starts[P.n_seqs], share = share_of(total, b.grid);
-  const long long a = (lead ? 0 : b.starts[i]) + (kvh * it.count + u) * it.units<KIND>() + K::W_ITEM;
-  const int c0 = quotient(a, share), c1 = quotient(a + (long long)(it.T - 1) * K::W_TILE, share);
-  Parts p;
-  if (c0 == c1) {
-    p.o = lead ? P.lead_o : P.own_o;
-    p.l = lead ? P.lead_lse : P.own_lse;
-    p.first = row;
-    p.step = 0;
-    p.n = 1;
-  } else {   // the item goes on behind CTA c0's share (slot 1), began before the others' (slot 0)
-    p.o = b.slot_o;
-    p.l = b.slot_lse;
-    p.first = 2ll * c0 * K::SLOT + slot_row<KIND>(P, tt, gh);
-    p.step = 2ll * K::SLOT;
-    p.n = c1 - c0 + 1;
-  }
-  return p;
+__device__ __forceinline__ Parts slot_parts(const ShareBuf& b, int slot_rows, int cta, int n, int row) {
+  // the item goes on behind the first CTA's share (slot 1), began before the others' (slot 0)
+  return {b.slot_o, b.slot_lse, 2ll * cta * slot_rows + row, 2ll * slot_rows, slot_rows, n};
 }
 template <bool BF16>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ SeqProb P) {
-  wait_for_predecessor();
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= (long long)P.total_q * P.Hq) return;
-  const int token = (int)((uint32_t)row / (uint32_t)P.Hq), head = (int)((uint32_t)row % (uint32_t)P.Hq);
-  const int i = seq_of_token(P, token);
-  const SeqInfo s = seq_info(P, i, nullptr);
-  if (token < s.q0 || token >= s.q0 + s.Lq) return;   // behind the last sequence
-  Parts parts[2];
-  parts[1] = takes<KIND_FEW>(P, s.Lq) ? parts_of<KIND_FEW>(P, P.few, false, s, i, token, head, row)
-                                      : parts_of<KIND_MANY>(P, P.many, false, s, i, token, head, row);
-  if (P.shared > 0) {
-    parts[0] = takes<KIND_FEW>(P, P.total_q) ? parts_of<KIND_FEW>(P, P.few, true, s, i, token, head, row)
-                                             : parts_of<KIND_MANY>(P, P.many, true, s, i, token, head, row);
-  } else {
-    parts[0].n = 0;
-    if (parts[1].n == 1) return;   // final already
-  }
-  // part c of the first CTA lies one slot further than `first` says
-  auto at = [&](const Parts& p, int c) { return p.first + c * p.step + (p.n > 1 && c == 0 ? p.step / 2 : 0); };
+__device__ __forceinline__ void join_row(const SeqProb& P, const Parts& a, const Parts& b, int token, int head, int lane) {
+  auto at = [&](const Parts& p, int c) { return p.first + c * p.step + (c == 0 ? p.back : 0); };
   float M = -INFINITY;
-#pragma unroll
-  for (int g = 0; g < 2; ++g)
-    for (int c = lane; c < parts[g].n; c += 32) M = fmaxf(M, parts[g].l[at(parts[g], c)]);
+  for (int c = lane; c < a.n; c += 32) M = fmaxf(M, a.l[at(a, c)]);
+  for (int c = lane; c < b.n; c += 32) M = fmaxf(M, b.l[at(b, c)]);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
   float sum = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (M != -INFINITY) {
-#pragma unroll
-    for (int g = 0; g < 2; ++g)
+  auto add = [&](const Parts& p) {
 #pragma unroll 4
-      for (int c = 0; c < parts[g].n; ++c) {
-        const long long k = at(parts[g], c);
-        const float l = parts[g].l[k];
-        const float4 x = reinterpret_cast<const float4*>(parts[g].o + k * D)[lane];
-        const float w = l == -INFINITY ? 0.0f : exp2f(l - M);   // 0: saw no key, all zeros
-        sum += w;
-        acc.x = fmaf(w, x.x, acc.x);
-        acc.y = fmaf(w, x.y, acc.y);
-        acc.z = fmaf(w, x.z, acc.z);
-        acc.w = fmaf(w, x.w, acc.w);
-      }
-  }
+    for (int c = 0; c < p.n; ++c) {
+      const long long k = at(p, c);
+      const float l = p.l[k];
+      const float4 x = reinterpret_cast<const float4*>(p.o + k * D)[lane];
+      const float w = l == -INFINITY ? 0.0f : exp2f(l - M);   // 0: saw no key, all zeros
+      sum += w;
+      acc.x = fmaf(w, x.x, acc.x);
+      acc.y = fmaf(w, x.y, acc.y);
+      acc.z = fmaf(w, x.z, acc.z);
+      acc.w = fmaf(w, x.w, acc.w);
+    }
+  };
+  add(a);
+  add(b);
   const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
   const uint2 out = make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
   *reinterpret_cast<uint2*>(P.o + token * P.o_tok + head * P.o_head + 8 * lane) = out;
-  if (lane == 0 && P.lse != nullptr) P.lse[row] = sum != 0.0f ? (M + log2f(sum)) * LN2 : -INFINITY;
+  if (lane == 0 && P.lse != nullptr)
+    P.lse[(long long)token * P.Hq + head] = sum != 0.0f ? (M + log2f(sum)) * LN2 : -INFINITY;
+}
+
+// No shared region: only the rows of items that were split, a CTA's slot per
+// grid row, 8 rows of it per block; KIND_MANY's CTAs first.
+template <bool BF16>
+__global__ void __launch_bounds__(256) join_items_kernel(const __grid_constant__ SeqProb P) {
+  wait_for_predecessor();
+  const bool few = blockIdx.x >= P.many.grid * (SLOT_ROWS / 8);
+  const ShareBuf& b = few ? P.few : P.many;
+  const int slot_rows = few ? FEW_ROWS : SLOT_ROWS, blk = blockIdx.x - (few ? P.many.grid * (SLOT_ROWS / 8) : 0);
+  const int cta = blk / (slot_rows / 8), row = blk % (slot_rows / 8) * 8 + (threadIdx.x >> 5);
+  const SplitItem it = b.split[cta];
+  if (it.parts == 0) return;
+  // the row's token and head, if it has any
+  const int r = few ? row : row & 127, t = over_G(P, r), gh = r - t * P.G;
+  const int tt = few ? t : t + (row >> 7) * P.TQ;
+  if ((!few && t >= P.TQ) || tt >= it.tokens) return;
+  join_row<BF16>(P, slot_parts(b, slot_rows, cta, it.parts, row), Parts{}, it.token + tt, it.kvh * P.G + gh, threadIdx.x & 31);
+}
+
+// With a shared region: every row has a result of it and one of its own
+// region, each whole or split.
+template <int KIND>
+__device__ __forceinline__ Parts parts_of(const SeqProb& P, const ShareBuf& b, bool lead, const SeqInfo& s, int i, int token,
+                                          int kvh, int gh, long long row) {
+  using K = Kind<KIND>;
+  const Items<KIND> it = items_of<KIND>(P, lead, s);
+  const int t = lead ? token : token - s.q0, per = K::tokens_per_item(P), u = t / per;
+  const long long share = share_of(b.starts[P.n_seqs], b.grid);
+  const long long a = (lead ? 0 : b.starts[i]) + kvh * it.all() + it.before(u) + K::W_ITEM;
+  const int c0 = quotient(a, share), c1 = quotient(a + (long long)(it.tiles(u) - 1) * K::TILE, share);
+  if (c0 == c1) return {lead ? P.lead_o : P.own_o, lead ? P.lead_lse : P.own_lse, row, 0, 0, 1};
+  return slot_parts(b, K::SLOT, c0, c1 - c0 + 1, slot_row<KIND>(P, t - u * per, gh));
+}
+template <bool BF16>
+__global__ void __launch_bounds__(256) join_rows_kernel(const __grid_constant__ SeqProb P) {
+  wait_for_predecessor();
+  const uint32_t row = blockIdx.x * 8u + (threadIdx.x >> 5);
+  if (row >= (uint32_t)P.total_q * P.Hq) return;
+  const int token = row / (uint32_t)P.Hq, head = row % (uint32_t)P.Hq, kvh = head / P.G, gh = head - kvh * P.G;
+  const int i = seq_of_token(P, token);
+  const SeqInfo s = seq_info(P, i, nullptr);
+  if (token < s.q0 || token >= s.q0 + s.Lq) return;   // behind the last sequence
+  const Parts own = takes<KIND_FEW>(P, s.Lq) ? parts_of<KIND_FEW>(P, P.few, false, s, i, token, kvh, gh, row)
+                                             : parts_of<KIND_MANY>(P, P.many, false, s, i, token, kvh, gh, row);
+  const Parts lead = takes<KIND_FEW>(P, P.total_q) ? parts_of<KIND_FEW>(P, P.few, true, s, i, token, kvh, gh, row)
+                                                   : parts_of<KIND_MANY>(P, P.many, true, s, i, token, kvh, gh, row);
+  join_row<BF16>(P, lead, own, token, head, threadIdx.x & 31);
 }
 
 template <bool BF16>
@@ -844,19 +894,23 @@ cudaError_t launch(const SeqProb& p, const SeqMaps& m, void* ws,
   if (p.many.grid > 0) {
     const int smem = Smem::BYTES + 1024;   // > half the SM: one CTA per SM owns all 512 TMEM columns
     auto kern = seq_attn_kernel<BF16>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static OncePerDevice once;
+    e = once.run([&] {
+      cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaFuncAttributes fa;   // the setmaxnreg split needs exactly LAUNCH_REGS at launch
+      if (r == cudaSuccess) r = cudaFuncGetAttributes(&fa, kern);
+      return r == cudaSuccess && fa.numRegs != LAUNCH_REGS ? cudaErrorInvalidConfiguration : r;
+    });
     if (e != cudaSuccess) return e;
-    cudaFuncAttributes fa;   // the setmaxnreg split needs exactly LAUNCH_REGS at launch
-    e = cudaFuncGetAttributes(&fa, kern);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs != LAUNCH_REGS) return cudaErrorInvalidConfiguration;
     e = launch_after(!first, kern, p.many.grid, NUM_THREADS, smem, st, p, m.q, m.k, m.v, static_cast<WsHeader*>(ws),
                      wait_limit());
     if (e != cudaSuccess) return e;
   }
   if (!p.split) return cudaSuccess;
+  if (p.shared == 0)
+    return launch_after(true, join_items_kernel<BF16>, p.many.grid * (SLOT_ROWS / 8) + p.few.grid * (FEW_ROWS / 8), 256, 0, st, p);
   const long long rows = (long long)p.total_q * p.Hq;
-  return launch_after(true, combine_kernel<BF16>, (unsigned)((rows + 7) / 8), 256, 0, st, p);
+  return launch_after(true, join_rows_kernel<BF16>, (unsigned)((rows + 7) / 8), 256, 0, st, p);
 }
 
 }  // namespace

@@ -4,6 +4,7 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <atomic>
 #include <cstdint>
 
 #include "ra_serve.h"
@@ -105,23 +106,40 @@ cudaError_t launch_after(bool overlap, void (*kern)(Params...), unsigned grid, u
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// What a kernel needs set on each device before its first launch there (a
+// device reset drops it, as it drops the caller's memory).
+struct OncePerDevice {
+  std::atomic<uint64_t> done{0};   // one bit per device; from the 64th on it is set every time
+  template <class F>
+  cudaError_t run(F set) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+    e = set();
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+    return e;
+  }
+};
+
 // ---------------------------------------------------------------- shares
 // The two kernels a call may use.  KIND_MANY: 128-row query tiles on the
 // tensor-memory MMA, items of two tiles.  KIND_FEW: at most FEW_ROWS rows over
 // pages, one item per sequence and key head, on the warp-level MMA.
-// All items' key tiles are laid end to end, W_ITEM units for an item and
-// W_TILE for each of its tiles, and cut into one share per CTA.
+// All items are laid end to end, W_ITEM units for an item and one for each
+// key it sees, and cut into one share per CTA.  A key tile goes to the CTA in
+// whose share its first unit lies.
 enum : int { KIND_MANY = 0, KIND_FEW = 1 };
 template <int KIND>
 struct Kind;
 template <>
 struct Kind<KIND_MANY> {
-  static constexpr int TILE_KEYS = KEYS, W_ITEM = 2, W_TILE = 2, SLOT = SLOT_ROWS;
+  static constexpr int TILE = KEYS, W_ITEM = 128, SLOT = SLOT_ROWS;
   __device__ static __forceinline__ int tokens_per_item(const SeqProb& P) { return 2 * P.TQ; }
 };
 template <>
 struct Kind<KIND_FEW> {
-  static constexpr int TILE_KEYS = FEW_KEYS, W_ITEM = 5, W_TILE = 2, SLOT = FEW_ROWS;
+  static constexpr int TILE = FEW_KEYS, W_ITEM = 160, SLOT = FEW_ROWS;
   __device__ static __forceinline__ int tokens_per_item(const SeqProb& P) { return FEW_ROWS; }
 };
 
@@ -138,26 +156,34 @@ __device__ __forceinline__ int slot_row(const SeqProb& P, int tt, int gh) {
 }
 
 // The items of one sequence's own region, or of the shared region: `count`
-// per key head, T key tiles each (at least one, so that rows without keys are
-// written too).
+// per key head.  Item u sees span(u) keys (at least one is counted, so that
+// rows without keys are written too); where the mask is causal that grows by
+// `step` tokens from item to item.
+template <int KIND>
 struct Items {
-  int count, T;
-  template <int KIND>
-  __device__ __forceinline__ long long units() const {
-    return Kind<KIND>::W_ITEM + (long long)T * Kind<KIND>::W_TILE;
+  int count, base, step, tokens;
+  __device__ __forceinline__ int span(int u) const {
+    return max(1, base + (step ? (int)min((long long)(u + 1) * step, (long long)tokens) : 0));
+  }
+  __device__ __forceinline__ int tiles(int u) const { return ceil_div(span(u), Kind<KIND>::TILE); }
+  // units before item u < count
+  __device__ __forceinline__ long long before(int u) const {
+    return (long long)u * (Kind<KIND>::W_ITEM + (step ? base : max(1, base))) + (long long)step * u * (u + 1) / 2;
+  }
+  __device__ __forceinline__ long long all() const {
+    return count == 0 ? 0 : before(count - 1) + Kind<KIND>::W_ITEM + span(count - 1);
   }
 };
 template <int KIND>
-__device__ __forceinline__ Items items_of(const SeqProb& P, int tokens, int keys) {
-  Items i;
-  i.count = takes<KIND>(P, tokens) ? ceil_div(tokens, Kind<KIND>::tokens_per_item(P)) : 0;
-  i.T = max(1, ceil_div(keys, Kind<KIND>::TILE_KEYS));
+__device__ __forceinline__ Items<KIND> items_of(const SeqProb& P, bool lead, const SeqInfo& s) {
+  Items<KIND> i;
+  i.tokens = lead ? P.total_q : s.Lq;
+  const int per = Kind<KIND>::tokens_per_item(P);
+  i.count = takes<KIND>(P, i.tokens) ? ceil_div(i.tokens, per) : 0;
+  const bool grows = P.causal && !lead;
+  i.base = lead ? P.shared : grows ? max(0, s.off) : s.len;
+  i.step = grows ? per : 0;
   return i;
-}
-template <int KIND>
-__device__ __forceinline__ long long units_of(const SeqProb& P, int tokens, int keys) {
-  const Items i = items_of<KIND>(P, tokens, keys);
-  return i.units<KIND>() * i.count * P.Hkv;
 }
 
 // a / b for a quotient that fits an int; mostly 32-bit.
@@ -165,11 +191,11 @@ __device__ __forceinline__ int quotient(long long a, long long b) {
   return (a | b) >> 32 == 0 ? (int)((uint32_t)a / (uint32_t)b) : (int)(a / b);
 }
 
-// A CTA's share of all units: at least an item of one tile, so that every CTA
-// between an item's first and last holds one of its tiles.
+// A CTA's share of all units: more than a tile, so that every CTA between an
+// item's first and last holds one of its tiles.
 __device__ __forceinline__ long long share_of(long long total, int ctas) {
   const long long t = total + ctas - 1;
-  return max(t >> 32 == 0 ? (long long)((uint32_t)t / (uint32_t)ctas) : t / ctas, 7ll);
+  return max(t >> 32 == 0 ? (long long)((uint32_t)t / (uint32_t)ctas) : t / ctas, 320ll);
 }
 
 // In shared memory: the plan of one CTA.
@@ -190,10 +216,10 @@ __device__ void plan_shares(const SeqProb& P, SharePlan& plan, DeviceErr* err) {
   const int per = ceil_div(P.n_seqs, THREADS);
   const int i0 = min(P.n_seqs, tid * per), i1 = min(P.n_seqs, i0 + per);
   long long sum = 0, best = -1;
-  SeqInfo s;
+  SeqInfo s{};
   for (int i = i0; i < i1; ++i) {
     s = seq_info(P, i, err);
-    sum += units_of<KIND>(P, s.Lq, s.len);
+    sum += items_of<KIND>(P, false, s).all() * P.Hkv;
     // the longest sequence, the first of them, gives the shared pages
     best = max(best, ((long long)s.L << 32) | (uint32_t)(0x7fffffff - i));
   }
@@ -208,7 +234,7 @@ __device__ void plan_shares(const SeqProb& P, SharePlan& plan, DeviceErr* err) {
   if (lane == 0) plan.best[warp] = best;
   if (tid == 0) plan.first_seq = -1;
   __syncthreads();
-  const long long lead = P.shared > 0 ? units_of<KIND>(P, P.total_q, P.shared) : 0;
+  const long long lead = P.shared > 0 ? items_of<KIND>(P, true, s).all() * P.Hkv : 0;
   long long total = lead, at = lead + incl - sum;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
@@ -230,7 +256,7 @@ __device__ void plan_shares(const SeqProb& P, SharePlan& plan, DeviceErr* err) {
   if (blockIdx.x == 0 || (mine >= at && mine < at + sum)) {
     for (int i = i0; i < i1; ++i) {
       if (per > 1) s = seq_info(P, i, nullptr);
-      const long long n = units_of<KIND>(P, s.Lq, s.len);
+      const long long n = items_of<KIND>(P, false, s).all() * P.Hkv;
       if (blockIdx.x == 0) b.starts[i] = at;
       if (mine >= at && mine < at + n) {
         plan.first_seq = i;
@@ -242,78 +268,100 @@ __device__ void plan_shares(const SeqProb& P, SharePlan& plan, DeviceErr* err) {
   __syncthreads();
 }
 
+template <int KIND>
 struct ShareWalk {
   long long at, end;     // the share
   long long start;       // first unit of the next item
-  int seq, item;         // sequence (-1: the shared region) and item in it
+  int seq, kvh, u;       // sequence (-1: the shared region), key head and item of that
   int known;             // the sequence that `s` and `it` describe (-2: none)
   SeqInfo s;
-  Items it;
+  Items<KIND> it;
 };
 struct SharePart {
   int lead, tokens;      // the shared region?; the query tokens of the sequence (of all)
   int kvh, item;
   int t0, t1;            // key tiles
   int out, slot;
+  int parts;             // OUT_SLOT, slot 1: the CTAs that the item is spread over
 };
 
 template <int KIND>
-__device__ __forceinline__ void know(const SeqProb& P, ShareWalk& w, DeviceErr* err) {
+__device__ __forceinline__ void know(const SeqProb& P, ShareWalk<KIND>& w, DeviceErr* err) {
   if (w.known == w.seq) return;
   if (w.seq >= 0) w.s = seq_info(P, w.seq, err);
-  w.it = w.seq < 0 ? items_of<KIND>(P, P.total_q, P.shared) : items_of<KIND>(P, w.s.Lq, w.s.len);
+  w.it = items_of<KIND>(P, w.seq < 0, w.s);
   w.known = w.seq;
 }
 template <int KIND>
-__device__ __forceinline__ void start_walk(const SeqProb& P, const SharePlan& plan, ShareWalk& w) {
+__device__ __forceinline__ void start_walk(const SeqProb& P, const SharePlan& plan, ShareWalk<KIND>& w) {
   const long long share = share_of(plan.total, gridDim.x);
   w.at = share * blockIdx.x;
   w.end = min(plan.total, w.at + share);
   w.seq = plan.first_seq;
   w.start = w.seq < 0 ? 0 : plan.first_start;
-  w.item = 0;
+  w.kvh = w.u = 0;
   w.known = -2;
+  w.s = SeqInfo{};
   if (w.at >= w.end) {
     w.start = w.end;
     return;
   }
   if (w.seq < 0 && P.shared == 0) w.seq = 0;
   know<KIND>(P, w, nullptr);
-  w.item = quotient(w.at - w.start, w.it.units<KIND>());
-  w.start += w.item * w.it.units<KIND>();
+  if (w.it.count == 0) return;
+  const long long all = w.it.all();
+  w.kvh = quotient(w.at - w.start, all);
+  w.start += w.kvh * all;
+  int lo = 0, hi = w.it.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (w.it.before(mid) <= w.at - w.start) lo = mid; else hi = mid - 1;
+  }
+  w.u = lo;
+  w.start += w.it.before(lo);
 }
 // The next part of the share; false at its end.
 template <int KIND>
-__device__ __forceinline__ bool next_share_part(const SeqProb& P, ShareWalk& w, SharePart& p, DeviceErr* err) {
+__device__ __forceinline__ bool next_share_part(const SeqProb& P, const SharePlan& plan, ShareWalk<KIND>& w, SharePart& p,
+                                                DeviceErr* err) {
   using K = Kind<KIND>;
   while (w.start < w.end && w.seq < P.n_seqs) {
     know<KIND>(P, w, err);
-    if (w.item >= w.it.count * P.Hkv) {
+    if (w.u >= w.it.count) {
+      w.u = 0;
+      ++w.kvh;
+    }
+    if (w.kvh >= P.Hkv || w.it.count == 0) {
       ++w.seq;
-      w.item = 0;
+      w.kvh = w.u = 0;
       continue;
     }
     const long long a = w.start + K::W_ITEM;   // the item's first tile
-    const int item = w.item, T = w.it.T;
-    w.start = a + (long long)T * K::W_TILE;
-    ++w.item;
-    // a tile is this CTA's if its first unit lies in the share
-    auto tile_at = [&](long long x) {
-      return (int)(((uint32_t)max(0ll, min(x - a, (long long)T * K::W_TILE)) + K::W_TILE - 1) / K::W_TILE);
-    };
+    const int span = w.it.span(w.u), T = ceil_div(span, K::TILE);
+    w.start = a + span;
+    p.item = w.u++;
+    auto tile_at = [&](long long x) { return ((int)max(0ll, min(x - a, (long long)T * K::TILE)) + K::TILE - 1) / K::TILE; };
     p.t0 = tile_at(w.at);
     p.t1 = tile_at(w.end);
     if (p.t0 >= p.t1) continue;
     p.lead = w.seq < 0;
-    p.tokens = p.lead ? P.total_q : w.s.Lq;
-    p.kvh = item / w.it.count;
-    p.item = item - p.kvh * w.it.count;
+    p.tokens = w.it.tokens;
+    p.kvh = w.kvh;
     p.slot = 2 * blockIdx.x + (p.t0 > 0 ? 0 : 1);   // 0: began in an earlier CTA, 1: goes on in a later one
     p.out = (p.t0 > 0 || p.t1 < T) ? OUT_SLOT : (P.shared == 0 ? OUT_FINAL : (p.lead ? OUT_LEAD : OUT_OWN));
+    p.parts = quotient(a + (long long)(T - 1) * K::TILE, w.end - w.at) - (int)blockIdx.x + 1;
     return true;
   }
   return false;
 }
+
+// What the join needs to know of an item that goes on behind a CTA's share
+// (no shared region: rows are joined by item).
+struct SplitItem {
+  int parts;             // CTAs it is spread over; 0: none goes on
+  int token, tokens;     // its first token and how many
+  int kvh;
+};
 
 // ---------------------------------------------------------------- rows
 // How many keys of the shared region a query token sees.

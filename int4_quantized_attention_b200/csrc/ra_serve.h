@@ -19,11 +19,14 @@ constexpr int SLOT_ROWS = 256;   // query rows of a work item: two 128-row tiles
 // pages of a cache (paged = 1), there in two regions: the first `shared`
 // tokens, taken from one sequence for the whole batch, and each sequence's
 // own tokens behind them.
+struct SplitItem;
+
 // One kernel's shares of the key tiles (split calls).
 struct ShareBuf {
   int grid;                      // CTAs; 0: not launched
   long long* starts;             // first unit of each sequence, [n_seqs + 1]
   float *slot_o, *slot_lse;      // [grid][2][rows of a slot](x 128)
+  SplitItem* split;              // [grid], the item that goes on behind each share
 };
 
 struct SeqProb {
@@ -57,7 +60,7 @@ struct SeqProb {
 
 // Workspace of a split call (after the 256-byte header).
 struct SeqWs {
-  size_t many_starts, many_o, many_lse, few_starts, few_o, few_lse, lead_o, lead_lse, own_o, own_lse, total;
+  size_t many_starts, many_split, many_o, many_lse, few_starts, few_split, few_o, few_lse, lead_o, lead_lse, own_o, own_lse, total;
 };
 inline SeqWs seq_ws(int n_seqs, long long total_q, int Hq, int shared, int many, int few) {
   SeqWs L;
@@ -70,9 +73,11 @@ inline SeqWs seq_ws(int n_seqs, long long total_q, int Hq, int shared, int many,
   const size_t rows = shared ? (size_t)total_q * Hq : 0, starts = sizeof(long long) * ((size_t)n_seqs + 1);
   const size_t many_rows = (size_t)many * 2 * SLOT_ROWS, few_rows = (size_t)few * 2 * FEW_ROWS;
   L.many_starts = take(many ? starts : 0);
+  L.many_split = take(16 * (size_t)many);
   L.many_o = take(many_rows * D * sizeof(float));
   L.many_lse = take(many_rows * sizeof(float));
   L.few_starts = take(few ? starts : 0);
+  L.few_split = take(16 * (size_t)few);
   L.few_o = take(few_rows * D * sizeof(float));
   L.few_lse = take(few_rows * sizeof(float));
   L.lead_o = take(rows * D * sizeof(float));

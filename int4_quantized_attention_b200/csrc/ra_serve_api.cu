@@ -1,6 +1,7 @@
 // ra_serve_api.cu -- host side of the packed-sequence and paged-cache calls of
 // include/rotate_attn.h: argument checks, tensor maps, workspaces and the
 // choice between whole work items and split keys.  No allocation.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -102,9 +103,12 @@ float log2_scale(double scale) {
 }
 
 ra_status sm_count(int* out) {
+  static std::atomic<int> known[64];   // per device; 0: not asked yet
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev < 64 && (*out = known[dev].load(std::memory_order_relaxed)) != 0) return RA_OK;
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < 64) known[dev].store(*out, std::memory_order_relaxed);
   return e == cudaSuccess ? RA_OK : cuda_fail(e, "device query");
 }
 
@@ -240,6 +244,8 @@ void bind_ws(ra::SeqProb* P, int many, int few, void* ws) {
   char* b = static_cast<char*>(ws);
   auto floats = [&](size_t o) { return reinterpret_cast<float*>(b + o); };
   P->many.starts = reinterpret_cast<long long*>(b + L.many_starts);
+  P->many.split = reinterpret_cast<ra::SplitItem*>(b + L.many_split);
+  P->few.split = reinterpret_cast<ra::SplitItem*>(b + L.few_split);
   P->many.slot_o = floats(L.many_o);
   P->many.slot_lse = floats(L.many_lse);
   P->few.starts = reinterpret_cast<long long*>(b + L.few_starts);
@@ -500,8 +506,8 @@ ra_status ra_cache_attention_fwd(const ra_cache_problem* p, const ra_cache* c, c
   const cuuint64_t outer[3] = {(cuuint64_t)p->page_size, (cuuint64_t)p->Hkv, (cuuint64_t)p->n_pages};
   const cuuint64_t stride[3] = {256, (cuuint64_t)P.v_head, (cuuint64_t)P.v_page};
   const cuuint32_t box[3] = {(cuuint32_t)p->page_size, 1, 1};
-  if (!q_map(&m, P, q, a->q_token, a->q_head) || !make_map(&m.k, P.bf16, kb, outer, stride, box) ||
-      !make_map(&m.v, P.bf16, vb, outer, stride, box))
+  if (many && (!q_map(&m, P, q, a->q_token, a->q_head) || !make_map(&m.k, P.bf16, kb, outer, stride, box) ||
+               !make_map(&m.v, P.bf16, vb, outer, stride, box)))
     return fail(RA_ERR_CUDA, "tensor map of q or the pool");
   const cudaError_t e = ra::launch_seq_attention(P, m, ws, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RA_OK : cuda_fail(e, "cache attention launch");
