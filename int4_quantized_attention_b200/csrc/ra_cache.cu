@@ -48,56 +48,58 @@ __device__ __forceinline__ int read_peer(const int* p, int rank) {
   return v;
 }
 
+struct Sums {
+  int need, pages, flags;
+};
 struct Shared {
-  int warp[32];
-  int total;
-  int bad;
-  int cta[CL];
+  int need[32], pages[32], flags[32];   // per warp
+  Sums total;                           // this CTA's
 };
 
-// Exclusive prefix of x over the cluster's threads, in thread order of CTA 0,
-// 1, ...; `all` gets the total.  Every thread of the cluster calls it.
-__device__ int cluster_prefix(int x, Shared* sh, int& all) {
+// Of every thread's `need` and `pages` the exclusive prefix over the cluster's
+// threads (in thread order of CTA 0, 1, ...), all of them together, and the
+// OR of the flags.  Every thread of the cluster calls it; one exchange for all
+// three, since what a state call costs are its cluster barriers.
+struct Scan {
+  Sums before, all;
+};
+__device__ Scan cluster_scan(int need, int pages, int flags, Shared* sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int incl = x;
+  int a = need, b = pages;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += y;
+    const int x = __shfl_up_sync(0xffffffffu, a, d), y = __shfl_up_sync(0xffffffffu, b, d);
+    if (lane >= d) a += x, b += y;
   }
-  if (lane == 31) sh->warp[warp] = incl;
+  flags = __reduce_or_sync(0xffffffffu, flags);
+  if (lane == 31) sh->need[warp] = a, sh->pages[warp] = b, sh->flags[warp] = flags;
   __syncthreads();
   if (warp == 0) {
-    const int v = sh->warp[lane];
-    int run = v;
+    const int v = sh->need[lane], w = sh->pages[lane], f = __reduce_or_sync(0xffffffffu, sh->flags[lane]);
+    int x = v, y = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, run, d);
-      if (lane >= d) run += y;
+      const int p = __shfl_up_sync(0xffffffffu, x, d), q = __shfl_up_sync(0xffffffffu, y, d);
+      if (lane >= d) x += p, y += q;
     }
-    sh->warp[lane] = run - v;
-    if (lane == 31) sh->total = run;
+    sh->need[lane] = x - v;
+    sh->pages[lane] = y - w;
+    if (lane == 31) sh->total = {x, y, f};
   }
   cluster_barrier();
-  if (tid < CL) sh->cta[tid] = read_peer(&sh->total, tid);
-  cluster_barrier();   // no CTA reuses `total`, nor ends, before every peer has read it
-  int base = 0;
-  all = 0;
+  Scan r{};
 #pragma unroll
   for (int c = 0; c < CL; ++c) {
-    if (c < ctarank()) base += sh->cta[c];
-    all += sh->cta[c];
+    const int x = read_peer(&sh->total.need, c), y = read_peer(&sh->total.pages, c);
+    r.all.flags |= read_peer(&sh->total.flags, c);
+    if (c < ctarank()) r.before.need += x, r.before.pages += y;
+    r.all.need += x;
+    r.all.pages += y;
   }
-  const int out = base + sh->warp[warp] + incl - x;
-  __syncthreads();
-  return out;
-}
-
-// Whether any thread of the cluster says so; all threads call it.
-__device__ bool cluster_any(bool x, Shared* sh) {
-  int all;
-  cluster_prefix(x ? 1 : 0, sh, all);
-  return all != 0;
+  r.before.need += sh->need[warp] + a - need;
+  r.before.pages += sh->pages[warp] + b - pages;
+  cluster_barrier();   // no CTA reuses its sums, nor ends, before every peer has read them
+  return r;
 }
 
 struct Ws {
@@ -119,76 +121,84 @@ __device__ __forceinline__ bool row_ok(const CacheProb& c, int row) {
   return len >= 0 && (long long)len <= (long long)c.max_pages << c.page_shift;
 }
 
+enum : int { BAD = 1, TOO_MUCH = 2 };   // flags of a scan
+
 // Marks the rows of a list: rows named twice, or by both lists of a fork, are
-// found by the count.  -1 entries take no part.
-__device__ bool rows_unique(const CacheProb& c, const Ws& w, const int* rows, int n, const int* others, Shared* sh) {
+// found by the count.  -1 entries take no part.  Returns BAD or 0, by thread.
+__device__ int check_rows(const CacheProb& c, const Ws& w, const int* rows, int n, const int* others) {
   const int at = ctarank() * CT + threadIdx.x;
   for (int i = at; i < n; i += ALL) {
     if (rows[i] >= 0 && rows[i] < c.max_seqs) w.mark[rows[i]] = 0;
     if (others != nullptr && others[i] >= 0 && others[i] < c.max_seqs) w.mark[others[i]] = 0;
   }
   cluster_barrier();
-  bool bad = false;
+  int bad = 0;
   for (int i = at; i < n; i += ALL) {
     if (rows[i] == -1) continue;
-    if (!row_ok(c, rows[i])) bad = true;
-    else if (atomicAdd(&w.mark[rows[i]], 1) != 0) bad = true;
+    if (!row_ok(c, rows[i])) bad = BAD;
+    else if (atomicAdd(&w.mark[rows[i]], 1) != 0) bad = BAD;
   }
-  cluster_barrier();
-  if (others != nullptr)
+  if (others != nullptr) {
+    cluster_barrier();
     for (int i = at; i < n; i += ALL) {
       if (rows[i] == -1) continue;
-      if (!row_ok(c, others[i]) || w.mark[others[i]] != 0) bad = true;
+      if (!row_ok(c, others[i]) || w.mark[others[i]] != 0) bad = BAD;
     }
-  return !cluster_any(bad, sh);
+  }
+  return bad;
 }
 
-// The first `want` free pages, lowest first, into w.list; false (and nothing
-// changed) if there are fewer.
-__device__ bool lowest_free(const CacheProb& c, const Ws& w, int want, Shared* sh) {
-  const int per = (c.n_pages + ALL - 1) / ALL;
-  const int at = ctarank() * CT + threadIdx.x;
-  const int p0 = min(c.n_pages, at * per), p1 = min(c.n_pages, p0 + per);
-  int free_here = 0;
-  for (int p = p0; p < p1; ++p) free_here += c.refs[p] == 0;
-  int all;
-  int r = cluster_prefix(free_here, sh, all);
-  if (all < want) return false;
-  for (int p = p0; p < p1 && r < want; ++p)
-    if (c.refs[p] == 0) w.list[r++] = p;
-  cluster_barrier();
-  return true;
+// This thread's run of pages (consecutive, so that ranks ascend with numbers).
+struct Run {
+  int p0, p1;
+};
+__device__ __forceinline__ Run page_run(const CacheProb& c) {
+  const int per = (c.n_pages + ALL - 1) / ALL, at = ctarank() * CT + threadIdx.x;
+  return {min(c.n_pages, at * per), min(c.n_pages, at * per + per)};
+}
+__device__ __forceinline__ int count_free(const CacheProb& c, Run r) {
+  int n = 0;
+#pragma unroll 4
+  for (int p = r.p0; p < r.p1; ++p) n += c.refs[p] == 0;
+  return n;
+}
+// The first `want` free pages, lowest first, into w.list.
+__device__ __forceinline__ void list_free(const CacheProb& c, const Ws& w, Run r, int rank, int want) {
+  for (int p = r.p0; p < r.p1 && rank < want; ++p)
+    if (c.refs[p] == 0) w.list[rank++] = p;
 }
 
 __device__ __forceinline__ void report_once(WsHeader* h, uint32_t bit, uint32_t site) {
   if (ctarank() == 0 && threadIdx.x == 0) report(&h->err, bit, site);
 }
+// Whether a call has to be refused; says so.
+__device__ __forceinline__ bool refused(const Scan& s, WsHeader* h, uint32_t site) {
+  if (s.all.flags & BAD) report_once(h, DEVERR_BOUNDS, site);
+  else if ((s.all.flags & TOO_MUCH) || s.all.need > s.all.pages) report_once(h, DEVERR_FULL, site + 1);
+  else return false;
+  return true;
+}
 
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
     extend_kernel(CacheProb c, const int* __restrict__ seqs, const int* __restrict__ n_new, int n, Ws w) {
   __shared__ Shared sh;
-  if (!rows_unique(c, w, seqs, n, nullptr, &sh)) return report_once(w.hdr, DEVERR_BOUNDS, 0x5001);
+  int flags = check_rows(c, w, seqs, n, nullptr);
   // entries in list order, a run of consecutive ones per thread
   const int per = (n + ALL - 1) / ALL, at = ctarank() * CT + threadIdx.x;
   const int i0 = min(n, at * per), i1 = min(n, i0 + per);
   int need = 0;
-  bool bad = false, full = false;
   for (int i = i0; i < i1; ++i) {
-    if (seqs[i] == -1) continue;
+    if (seqs[i] == -1 || !row_ok(c, seqs[i])) continue;
     const int len = c.lens[seqs[i]], add = n_new[i];
-    if (add < 0) {
-      bad = true;
-    } else if ((long long)len + add > (long long)c.max_pages << c.page_shift) {
-      full = true;
-    } else {
-      need += pages_for(c, len + add) - pages_for(c, len);   // summed: at most max_seqs x max_pages < 2^31
-    }
+    if (add < 0) flags |= BAD;
+    else if ((long long)len + add > (long long)c.max_pages << c.page_shift) flags |= TOO_MUCH;
+    else need += pages_for(c, len + add) - pages_for(c, len);   // over distinct rows: at most max_seqs x max_pages < 2^31
   }
-  if (cluster_any(bad, &sh)) return report_once(w.hdr, DEVERR_BOUNDS, 0x5002);
-  if (cluster_any(full, &sh)) return report_once(w.hdr, DEVERR_FULL, 0x5003);
-  int want;
-  int r = cluster_prefix(need, &sh, want);
-  if (!lowest_free(c, w, want, &sh)) return report_once(w.hdr, DEVERR_FULL, 0x5004);
+  const Run run = page_run(c);
+  const Scan s = cluster_scan(need, count_free(c, run), flags, &sh);
+  if (refused(s, w.hdr, 0x5001)) return;
+  list_free(c, w, run, s.before.pages, s.all.need);
+  int r = s.before.need;
   for (int i = i0; i < i1; ++i) {
     w.rank[i] = r;
     if (seqs[i] != -1) r += pages_for(c, c.lens[seqs[i]] + n_new[i]) - pages_for(c, c.lens[seqs[i]]);
@@ -212,21 +222,21 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
     fork_kernel(CacheProb c, const int* __restrict__ parents, const int* __restrict__ children, int n, Ws w) {
   __shared__ Shared sh;
-  if (ctarank() == 0 && threadIdx.x == 0) w.jobs[0] = 0;   // nothing to copy if this call is refused
-  if (!rows_unique(c, w, children, n, parents, &sh)) return report_once(w.hdr, DEVERR_BOUNDS, 0x5011);
+  int flags = check_rows(c, w, children, n, parents);
   const int per = (n + ALL - 1) / ALL, at = ctarank() * CT + threadIdx.x;
+  if (at == 0) w.jobs[0] = 0;   // nothing to copy if this call is refused
   const int i0 = min(n, at * per), i1 = min(n, i0 + per);
   int need = 0;
-  bool bad = false;
   for (int i = i0; i < i1; ++i) {
-    if (children[i] == -1) continue;
-    bad |= c.lens[children[i]] != 0;
+    if (children[i] == -1 || !row_ok(c, children[i]) || !row_ok(c, parents[i])) continue;
+    if (c.lens[children[i]] != 0) flags |= BAD;
     need += (c.lens[parents[i]] & (c.page_size - 1)) != 0;
   }
-  if (cluster_any(bad, &sh)) return report_once(w.hdr, DEVERR_BOUNDS, 0x5012);
-  int want;
-  int r = cluster_prefix(need, &sh, want);
-  if (!lowest_free(c, w, want, &sh)) return report_once(w.hdr, DEVERR_FULL, 0x5013);
+  const Run run = page_run(c);
+  const Scan s = cluster_scan(need, count_free(c, run), flags, &sh);
+  if (refused(s, w.hdr, 0x5011)) return;
+  list_free(c, w, run, s.before.pages, s.all.need);
+  int r = s.before.need;
   for (int i = i0; i < i1; ++i) {
     w.rank[i] = r;
     if (children[i] != -1) r += (c.lens[parents[i]] & (c.page_size - 1)) != 0;
@@ -254,6 +264,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
         w.dst[w.rank[i]] = page;
         w.rows[w.rank[i]] = rest;
         if ((uint32_t)old >= (uint32_t)c.n_pages) {
+          w.src[w.rank[i]] = 0;
           w.rows[w.rank[i]] = 0;
           report(&w.hdr->err, DEVERR_BOUNDS, 0x5014);
         }
@@ -261,13 +272,13 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
       c.lens[child] = len;
     }
   }
-  if (ctarank() == 0 && threadIdx.x == 0) w.jobs[0] = want;
+  if (at == 0) w.jobs[0] = s.all.need;
 }
 
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
     free_kernel(CacheProb c, const int* __restrict__ seqs, int n, Ws w) {
   __shared__ Shared sh;
-  if (!rows_unique(c, w, seqs, n, nullptr, &sh)) return report_once(w.hdr, DEVERR_BOUNDS, 0x5021);
+  if (refused(cluster_scan(0, 0, check_rows(c, w, seqs, n, nullptr), &sh), w.hdr, 0x5021)) return;
   const int lane = threadIdx.x & 31, at = ctarank() * CT + threadIdx.x;
   for (int i = at >> 5; i < n; i += ALL / 32) {
     const int row = seqs[i];
@@ -287,20 +298,21 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
 
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT) compact_kernel(CacheProb c, Ws w) {
   __shared__ Shared sh;
-  const int per = (c.n_pages + ALL - 1) / ALL, at = ctarank() * CT + threadIdx.x;
-  const int p0 = min(c.n_pages, at * per), p1 = min(c.n_pages, p0 + per);
-  int live = 0, holes = 0, total;
-  for (int p = p0; p < p1; ++p) live += c.refs[p] > 0;
-  cluster_prefix(live, &sh, total);
-  int movers = 0, n;
-  for (int p = p0; p < p1; ++p) {
-    const bool is = c.refs[p] > 0;
+  const int at = ctarank() * CT + threadIdx.x;
+  const Run run = page_run(c);
+  const int live = (run.p1 - run.p0) - count_free(c, run);
+  const int total = cluster_scan(0, live, 0, &sh).all.pages;
+  int holes = 0, movers = 0;
+  for (int p = run.p0; p < run.p1; ++p) {
+    const bool is = c.refs[p] != 0;
     holes += !is && p < total;
     movers += is && p >= total;
   }
-  int h = cluster_prefix(holes, &sh, n), m = cluster_prefix(movers, &sh, n);
-  for (int p = p0; p < p1; ++p) {
-    const bool is = c.refs[p] > 0;
+  const Scan s = cluster_scan(holes, movers, 0, &sh);
+  const int n = s.all.need;   // as many free pages below `total` as live ones above
+  int h = s.before.need, m = s.before.pages;
+  for (int p = run.p0; p < run.p1; ++p) {
+    const bool is = c.refs[p] != 0;
     w.map[p] = p;
     if (!is && p < total) w.dst[h++] = p;
     if (is && p >= total) w.src[m++] = p;

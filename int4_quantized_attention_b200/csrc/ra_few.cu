@@ -313,22 +313,24 @@ __global__ void __launch_bounds__(THREADS, FEW_CTAS) few_kernel(const __grid_con
     }
     __syncthreads();   // the ring is free for the next part
   }
+  // the kernel of many rows may still run: this grid ends after it, so that
+  // the join, which waits for this one, finds both results
+  wait_for_predecessor();
 }
 
 template <bool BF16>
-cudaError_t launch(const SeqProb& p, WsHeader* hdr, cudaStream_t st) {
+cudaError_t launch(const SeqProb& p, WsHeader* hdr, bool overlap, cudaStream_t st) {
   static OncePerDevice once;
   const cudaError_t e = once.run(
       [] { return cudaFuncSetAttribute(few_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, RING); });
   if (e != cudaSuccess) return e;
-  few_kernel<BF16><<<p.few.grid, THREADS, RING, st>>>(p, hdr);
-  return cudaGetLastError();
+  return launch_after(overlap, few_kernel<BF16>, p.few.grid, THREADS, RING, st, p, hdr);
 }
 
 }  // namespace
 
-cudaError_t launch_few_attention(const SeqProb& p, WsHeader* hdr, cudaStream_t st) {
-  return p.bf16 ? launch<true>(p, hdr, st) : launch<false>(p, hdr, st);
+cudaError_t launch_few_attention(const SeqProb& p, WsHeader* hdr, bool overlap, cudaStream_t st) {
+  return p.bf16 ? launch<true>(p, hdr, overlap, st) : launch<false>(p, hdr, overlap, st);
 }
 
 }  // namespace ra

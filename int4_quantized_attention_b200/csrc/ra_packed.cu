@@ -777,9 +777,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncwarp();
     mbar_wait(&bar[B_DRAIN + X], 0, limit_ns, err, 0x4306);
   }
-  // the kernel of few rows may still run: this grid ends after it, so that the
-  // joining kernel, which waits for this one, finds both results
-  wait_for_predecessor();
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
@@ -803,30 +800,41 @@ __device__ __forceinline__ Parts slot_parts(const ShareBuf& b, int slot_rows, in
 }
 template <bool BF16>
 __device__ __forceinline__ void join_row(const SeqProb& P, const Parts& a, const Parts& b, int token, int head, int lane) {
-  auto at = [&](const Parts& p, int c) { return p.first + c * p.step + (c == 0 ? p.back : 0); };
-  float M = -INFINITY;
-  for (int c = lane; c < a.n; c += 32) M = fmaxf(M, a.l[at(a, c)]);
-  for (int c = lane; c < b.n; c += 32) M = fmaxf(M, b.l[at(b, c)]);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  float sum = 0.0f;
+  float M = -INFINITY, sum = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  auto add = [&](const Parts& p) {
-#pragma unroll 4
-    for (int c = 0; c < p.n; ++c) {
-      const long long k = at(p, c);
-      const float l = p.l[k];
-      const float4 x = reinterpret_cast<const float4*>(p.o + k * D)[lane];
-      const float w = l == -INFINITY ? 0.0f : exp2f(l - M);   // 0: saw no key, all zeros
-      sum += w;
-      acc.x = fmaf(w, x.x, acc.x);
-      acc.y = fmaf(w, x.y, acc.y);
-      acc.z = fmaf(w, x.z, acc.z);
-      acc.w = fmaf(w, x.w, acc.w);
+  const int n = a.n + b.n;
+  // four parts at a time, all their loads before the first use
+  for (int c0 = 0; c0 < n; c0 += 4) {
+    float l[4];
+    float4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      l[k] = -INFINITY;
+      x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const int c = c0 + k;
+      if (c >= n) continue;
+      const Parts& p = c < a.n ? a : b;
+      const int d = c < a.n ? c : c - a.n;
+      const long long at = p.first + d * p.step + (d == 0 ? p.back : 0);
+      l[k] = p.l[at];
+      x[k] = reinterpret_cast<const float4*>(p.o + at * D)[lane];
     }
-  };
-  add(a);
-  add(b);
+    const float m = fmaxf(fmaxf(M, fmaxf(l[0], l[1])), fmaxf(l[2], l[3]));
+    if (l[0] == -INFINITY && l[1] == -INFINITY && l[2] == -INFINITY && l[3] == -INFINITY) continue;   // saw no key
+    const float old = exp2f(M - m);
+    M = m;
+    sum *= old;
+    acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float w = exp2f(l[k] - m);             // NaN stays NaN
+      sum += w;
+      acc.x = fmaf(w, x[k].x, acc.x);
+      acc.y = fmaf(w, x[k].y, acc.y);
+      acc.z = fmaf(w, x[k].z, acc.z);
+      acc.w = fmaf(w, x[k].w, acc.w);
+    }
+  }
   const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
   const uint2 out = make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
   *reinterpret_cast<uint2*>(P.o + token * P.o_tok + head * P.o_head + 8 * lane) = out;
@@ -853,44 +861,64 @@ __global__ void __launch_bounds__(256) join_items_kernel(const __grid_constant__
 }
 
 // With a shared region: every row has a result of it and one of its own
-// region, each whole or split.
+// region, each whole or split.  A block takes P.join_heads heads of one token,
+// whose sequence it looks up once.
 template <int KIND>
-__device__ __forceinline__ Parts parts_of(const SeqProb& P, const ShareBuf& b, bool lead, const SeqInfo& s, int i, int token,
-                                          int kvh, int gh, long long row) {
-  using K = Kind<KIND>;
-  const Items<KIND> it = items_of<KIND>(P, lead, s);
-  const int t = lead ? token : token - s.q0, per = K::tokens_per_item(P), u = t / per;
-  const long long share = share_of(b.starts[P.n_seqs], b.grid);
-  const long long a = (lead ? 0 : b.starts[i]) + kvh * it.all() + it.before(u) + K::W_ITEM;
-  const int c0 = quotient(a, share), c1 = quotient(a + (long long)(it.tiles(u) - 1) * K::TILE, share);
-  if (c0 == c1) return {lead ? P.lead_o : P.own_o, lead ? P.lead_lse : P.own_lse, row, 0, 0, 1};
-  return slot_parts(b, K::SLOT, c0, c1 - c0 + 1, slot_row<KIND>(P, t - u * per, gh));
+struct RegionParts {
+  long long first, all, share;   // first tile of the token's item at key head 0; units per key head
+  int tiles, row0, lead;
+  const ShareBuf* b;
+  __device__ __forceinline__ void find(const SeqProb& P, const ShareBuf& buf, bool is_lead, const SeqInfo& s, int i, int token) {
+    using K = Kind<KIND>;
+    const Items<KIND> it = items_of<KIND>(P, is_lead, s);
+    const int t = is_lead ? token : token - s.q0, per = K::tokens_per_item(P), u = t / per;
+    b = &buf;
+    lead = is_lead;
+    share = share_of(buf.starts[P.n_seqs], buf.grid);
+    all = it.all();
+    first = (is_lead ? 0 : buf.starts[i]) + it.before(u) + K::W_ITEM;
+    tiles = it.tiles(u);
+    row0 = slot_row<KIND>(P, t - u * per, 0);
+  }
+  __device__ __forceinline__ Parts parts(const SeqProb& P, int kvh, int gh, long long row) const {
+    using K = Kind<KIND>;
+    const long long a = first + kvh * all;
+    const int c0 = quotient(a, share), c1 = quotient(a + (long long)(tiles - 1) * K::TILE, share);
+    if (c0 == c1) return {lead ? P.lead_o : P.own_o, lead ? P.lead_lse : P.own_lse, row, 0, 0, 1};
+    return slot_parts(*b, K::SLOT, c0, c1 - c0 + 1, row0 + gh);
+  }
+};
+template <bool BF16, int LEAD, int OWN>
+__device__ __forceinline__ void join_token(const SeqProb& P, int token, int h0, const SeqInfo& s, int i) {
+  RegionParts<LEAD> lead;
+  RegionParts<OWN> own;
+  lead.find(P, LEAD == KIND_FEW ? P.few : P.many, true, s, i, token);
+  own.find(P, OWN == KIND_FEW ? P.few : P.many, false, s, i, token);
+  const int h1 = min(P.Hq, h0 + P.join_heads);
+  for (int head = h0 + (threadIdx.x >> 5); head < h1; head += 8) {
+    const int kvh = head / P.G, gh = head - kvh * P.G;
+    const long long row = (long long)token * P.Hq + head;
+    join_row<BF16>(P, lead.parts(P, kvh, gh, row), own.parts(P, kvh, gh, row), token, head, threadIdx.x & 31);
+  }
 }
 template <bool BF16>
 __global__ void __launch_bounds__(256) join_rows_kernel(const __grid_constant__ SeqProb P) {
-  wait_for_predecessor();
-  const uint32_t row = blockIdx.x * 8u + (threadIdx.x >> 5);
-  if (row >= (uint32_t)P.total_q * P.Hq) return;
-  const int token = row / (uint32_t)P.Hq, head = row % (uint32_t)P.Hq, kvh = head / P.G, gh = head - kvh * P.G;
+  const int per_token = ceil_div(P.Hq, P.join_heads), token = blockIdx.x / per_token;
+  const int h0 = (blockIdx.x - token * per_token) * P.join_heads;
   const int i = seq_of_token(P, token);
   const SeqInfo s = seq_info(P, i, nullptr);
+  wait_for_predecessor();
   if (token < s.q0 || token >= s.q0 + s.Lq) return;   // behind the last sequence
-  const Parts own = takes<KIND_FEW>(P, s.Lq) ? parts_of<KIND_FEW>(P, P.few, false, s, i, token, kvh, gh, row)
-                                             : parts_of<KIND_MANY>(P, P.many, false, s, i, token, kvh, gh, row);
-  const Parts lead = takes<KIND_FEW>(P, P.total_q) ? parts_of<KIND_FEW>(P, P.few, true, s, i, token, kvh, gh, row)
-                                                   : parts_of<KIND_MANY>(P, P.many, true, s, i, token, kvh, gh, row);
-  join_row<BF16>(P, lead, own, token, head, threadIdx.x & 31);
+  const bool lead_few = takes<KIND_FEW>(P, P.total_q), own_few = takes<KIND_FEW>(P, s.Lq);
+  if (lead_few) join_token<BF16, KIND_FEW, KIND_FEW>(P, token, h0, s, i);
+  else if (own_few) join_token<BF16, KIND_MANY, KIND_FEW>(P, token, h0, s, i);
+  else join_token<BF16, KIND_MANY, KIND_MANY>(P, token, h0, s, i);
 }
 
 template <bool BF16>
 cudaError_t launch(const SeqProb& p, const SeqMaps& m, void* ws,
                    cudaStream_t st) {
   cudaError_t e;
-  bool first = true;
-  if (p.few.grid > 0) {
-    if ((e = launch_few_attention(p, static_cast<WsHeader*>(ws), st)) != cudaSuccess) return e;
-    first = false;
-  }
   if (p.many.grid > 0) {
     const int smem = Smem::BYTES + 1024;   // > half the SM: one CTA per SM owns all 512 TMEM columns
     auto kern = seq_attn_kernel<BF16>;
@@ -902,15 +930,15 @@ cudaError_t launch(const SeqProb& p, const SeqMaps& m, void* ws,
       return r == cudaSuccess && fa.numRegs != LAUNCH_REGS ? cudaErrorInvalidConfiguration : r;
     });
     if (e != cudaSuccess) return e;
-    e = launch_after(!first, kern, p.many.grid, NUM_THREADS, smem, st, p, m.q, m.k, m.v, static_cast<WsHeader*>(ws),
+    e = launch_after(false, kern, p.many.grid, NUM_THREADS, smem, st, p, m.q, m.k, m.v, static_cast<WsHeader*>(ws),
                      wait_limit());
     if (e != cudaSuccess) return e;
   }
+  if (p.few.grid > 0 && (e = launch_few_attention(p, static_cast<WsHeader*>(ws), p.many.grid > 0, st)) != cudaSuccess) return e;
   if (!p.split) return cudaSuccess;
   if (p.shared == 0)
     return launch_after(true, join_items_kernel<BF16>, p.many.grid * (SLOT_ROWS / 8) + p.few.grid * (FEW_ROWS / 8), 256, 0, st, p);
-  const long long rows = (long long)p.total_q * p.Hq;
-  return launch_after(true, join_rows_kernel<BF16>, (unsigned)((rows + 7) / 8), 256, 0, st, p);
+  return launch_after(true, join_rows_kernel<BF16>, (unsigned)p.total_q * ceil_div(p.Hq, p.join_heads), 256, 0, st, p);
 }
 
 }  // namespace

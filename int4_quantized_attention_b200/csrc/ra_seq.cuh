@@ -213,6 +213,22 @@ template <int KIND, int THREADS>
 __device__ void plan_shares(const SeqProb& P, SharePlan& plan, DeviceErr* err) {
   const ShareBuf& b = KIND == KIND_FEW ? P.few : P.many;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (KIND == KIND_MANY && P.lead_only) {
+    // nothing depends on the lengths but whose pages are read: the first
+    // sequence's, if it reaches so far (others do below)
+    const SeqInfo first = seq_info(P, 0, nullptr);
+    if (first.L >= P.shared) {
+      if (tid == 0) {
+        plan.total = items_of<KIND>(P, true, first).all() * P.Hkv;
+        plan.first_seq = -1;
+        plan.lead_row = first.row;
+        plan.lead_len = first.L;
+        if (blockIdx.x == 0) b.starts[P.n_seqs] = plan.total;
+      }
+      __syncthreads();
+      return;
+    }
+  }
   const int per = ceil_div(P.n_seqs, THREADS);
   const int i0 = min(P.n_seqs, tid * per), i1 = min(P.n_seqs, i0 + per);
   long long sum = 0, best = -1;

@@ -53,6 +53,8 @@ struct SeqProb {
   const uint8_t* k;              // paged: as v
   int split;                     // 1: equal shares of key tiles per CTA, joined afterwards; 0: whole items
   long long items;               // split = 0: upper bound of work items
+  int join_heads;                // heads per block of the join by rows
+  int lead_only;                 // the kernel of many rows has the shared region alone
   ShareBuf many, few;            // the two kernels' shares
   float *lead_o, *lead_lse;      // shared > 0: [total_q * Hq](x 128), the shared region's result
   float *own_o, *own_lse;        // shared > 0: the own region's result
@@ -93,7 +95,7 @@ struct SeqMaps {
   CUtensorMap q, k, v;
 };
 
-cudaError_t launch_few_attention(const SeqProb& p, WsHeader* hdr, cudaStream_t st);
+cudaError_t launch_few_attention(const SeqProb& p, WsHeader* hdr, bool overlap, cudaStream_t st);
 cudaError_t launch_seq_attention(const SeqProb& p, const SeqMaps& m, void* ws, cudaStream_t st);
 
 }  // namespace ra

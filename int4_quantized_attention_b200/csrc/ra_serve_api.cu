@@ -500,8 +500,21 @@ ra_status ra_cache_attention_fwd(const ra_cache_problem* p, const ra_cache* c, c
   cache_kinds(a, P.G, false, &many, &few);
   bind_ws(&P, many ? SM_BOUND : 0, few ? ra::FEW_CTAS * SM_BOUND : 0, ws);
   cache_kinds(a, P.G, cu_q == nullptr, &many, &few);
+  // one head per warp while that fits the SMs at once; more per lookup else
+  P.join_heads = (long long)a->total_q * a->Hq <= 64ll * SM_BOUND ? 8 : 32;
+  P.lead_only = cu_q == nullptr && P.G <= ra::FEW_ROWS;
+  // A short shared region leaves SMs to the kernel of few rows, which runs
+  // beside it: LEAD_TILES of its key tiles per SM (a call of 61 sequences
+  // behind 2048 tokens: 51 us one after the other).
+  constexpr long long LEAD_TILES = 3;
   P.many.grid = many ? sms : 0;
-  P.few.grid = few ? ra::FEW_CTAS * sms : 0;
+  if (many && P.lead_only) {
+    const long long tiles = (long long)((a->shared + ra::KEYS - 1) / ra::KEYS) * p->Hkv *
+                            ((a->total_q + 2 * P.TQ - 1) / (2 * P.TQ));
+    const long long want = (tiles + LEAD_TILES - 1) / LEAD_TILES;
+    if (want < sms) P.many.grid = (int)want;
+  }
+  P.few.grid = few ? ra::FEW_CTAS * (P.many.grid < sms ? sms - P.many.grid : sms) : 0;
   ra::SeqMaps m;
   const cuuint64_t outer[3] = {(cuuint64_t)p->page_size, (cuuint64_t)p->Hkv, (cuuint64_t)p->n_pages};
   const cuuint64_t stride[3] = {256, (cuuint64_t)P.v_head, (cuuint64_t)P.v_page};

@@ -380,6 +380,28 @@ def test_wide_batch_long_prefix(hq, hkv):
     run_attention(c, m, list(range(150)), [1] * 150, hq, 4096)
 
 
+@pytest.mark.parametrize("shared", [0, 2048])
+def test_nan_queries_and_hidden_values(shared):
+    # drafted tokens: a value that only the later ones see; a NaN query beside others
+    c, m = filled([700, 40, 5], shared, 16, 2, BF16, seed=18)
+    own = [m.rows[i][(shared + n - 1) // 16] for i, n in ((0, 700), (1, 40))]
+    c.pool[1, 0, own[0], 1, (shared + 699) % 16, 3] = math.inf       # the last token's value
+    c.pool[1, 0, own[1], 0, (shared + 39) % 16, 100] = math.nan
+    q = rand(4, 9, 8, D, dtype=BF16)
+    q[8, 5, 0] = math.nan
+    cu = [0, 4, 8, 9]
+    o, lse = c.attention(0, q, ints([0, 1, 2]), cu_q=ints(cu), shared=shared, return_lse=True)
+    c.check()
+    assert bool(torch.isnan(o[8, 5]).all()) and bool(torch.isnan(lse[8, 5]))
+    q[8, 5, 0] = 0.0
+    o[8, 5], lse[8, 5] = 0.0, 0.0
+    want, wl, tol, tl = paged(c.pool, 0, m.rows, m.lens, q, [0, 1, 2], cu)
+    want[8, 5], wl[8, 5] = 0.0, 0.0
+    assert int((~torch.isfinite(want)).sum()) == 8                   # one channel of the 4 heads of two tokens
+    check(o, want, tol, "o")
+    check(lse, wl, tl, "lse")
+
+
 def test_layers_scale_and_peaked_scores():
     c, m = filled([500, 3], 128, 64, 2, F16, seed=14, layers=3)
     run_attention(c, m, [0, 1], [1, 1], 4, 128, layer=2, scale=0.5, gain=10.0)

@@ -168,6 +168,22 @@ def test_hidden_values_do_not_leak(op, dtype, heads):
     assert torch.equal(torch.nan_to_num(o3), torch.nan_to_num(o)) and torch.equal(torch.isnan(o3), torch.isnan(o))
 
 
+@pytest.mark.parametrize("nan_q", [True, False])
+def test_nan_rows_stay_nan_when_joined(op, nan_q):
+    # a NaN query, or a NaN key that every row sees: NaN whether or not the keys are split
+    q, k, v = inputs(12, 40, 9000, 2, 1, F16)
+    (q if nan_q else k)[3, 0, 9] = math.nan
+    o, lse = op.forward(q, k, v, ints([0, 40]), ints([0, 9000]), return_lse=True)
+    op.check()
+    bad = torch.zeros(40, 2, dtype=torch.bool, device="cuda")
+    if nan_q:
+        bad[3, 0] = True
+    else:
+        bad[:] = True
+    assert torch.equal(torch.isnan(o).all(-1), bad) and torch.equal(torch.isnan(o).any(-1), bad)
+    assert torch.equal(torch.isnan(lse), bad)
+
+
 def test_repeatable_captured_and_on_a_side_stream(op):
     lens = [260, 31, 1]
     q, k, v, cq, ck, o, lse = run_case(op, lens, [n + 400 for n in lens], 8, 2, BF16, True)
