@@ -44,7 +44,7 @@ struct Prob {
 // Workspace layout (all offsets 256-byte aligned).
 struct WsHeader {
   DeviceErr err;                // error word + first reporting site
-  uint32_t reserved0[2];
+  uint32_t ticket, leaving;     // packed attention: items given out, CTAs that have left (0 between calls)
   unsigned long long signature; // problem signature written by ra_prepare
 };
 

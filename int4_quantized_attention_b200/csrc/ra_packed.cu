@@ -15,8 +15,8 @@
 //
 // Every CTA is persistent (one per SM) and walks a list of segments: (item,
 // range of 128-key tiles).  Two ways to deal them out:
-//   whole items  one item per CTA in rounds, there and back; the last (longest)
-//                query tiles of each sequence come first.  Rows are final.
+//   whole items  one at a time to the CTA that is free, long ones first.  Rows
+//                are final.
 //   split        all key tiles of all items, laid end to end, are cut into
 //                equal shares, one per CTA, whatever the lengths are; an item
 //                that crosses a border leaves partial rows (fp32) that
@@ -189,31 +189,103 @@ __device__ __forceinline__ void fill_counts(const SeqProb& P, Seg& g, int t0, in
   g.nload = max(g.n[0], g.n[1]);
 }
 
-// Whole items: one per CTA in rounds, every other round backwards, since
-// items get shorter along the list and this evens out what each CTA gets.
-struct Rounds {
-  long long at;
+// Whole items go out one at a time: a CTA's first is its own number, each
+// later one the next that nobody has (a ticket in the workspace header, which
+// the last CTA to leave sets back).  Up to LPT_SEQS sequences the list runs from
+// the items with the most key tiles to those with the fewest, so that what
+// remains at the end is short; beyond that from the last query tiles of the
+// last sequence on.
+constexpr int LPT_SEQS = 128;
+struct WholeList {
+  Items<KIND_MANY> it[LPT_SEQS / 32];   // this lane's sequences: lane, lane + 32, ...
+  int pairs, most;                      // all pairs of query tiles; key tiles of the longest
   int round;
 };
-__device__ __forceinline__ void next_item(const SeqProb& P, Rounds& w, Seg& g, DeviceErr* err) {
-  const int per = 2 * P.TQ;
-  g.stop = 0;
-  while (w.at < P.items) {
-    const long long item = w.at + (w.round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    w.at += gridDim.x;
-    ++w.round;
-    if (item >= P.items) continue;
-    const int pr = (int)(P.items / P.Hkv - 1 - item / P.Hkv);
-    g.kvh = (int)(item % P.Hkv);
-    // sequence i's pairs lie at cu_q[i] / per + i and on (never more than
-    // the gap to the next sequence's first)
-    int lo = 0, hi = P.n_seqs - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (P.cu_q[mid] / per + mid <= pr) lo = mid; else hi = mid - 1;
+// How many of a sequence's pairs have at least T key tiles: its last ones.
+__device__ __forceinline__ int pairs_from(const Items<KIND_MANY>& it, int T) {
+  const int over = KEYS * (T - 1);      // keys that such a pair sees more than
+  if (it.count == 0 || it.span(it.count - 1) <= over) return 0;
+  if (it.step == 0 || over < it.base) return it.count;
+  return it.count - min((over - it.base) / it.step, it.count - 1);
+}
+__device__ __forceinline__ void start_list(const SeqProb& P, WholeList& w, int lane, DeviceErr* err) {
+  w.round = 0;
+  w.pairs = w.most = 0;
+  if (P.n_seqs > LPT_SEQS) return;
+#pragma unroll
+  for (int k = 0; k < LPT_SEQS / 32; ++k) {
+    const int i = lane + 32 * k;
+    w.it[k] = Items<KIND_MANY>{};
+    if (i >= P.n_seqs) continue;
+    w.it[k] = items_of<KIND_MANY>(P, false, seq_info(P, i, err));
+    w.pairs += w.it[k].count;
+    if (w.it[k].count > 0) w.most = max(w.most, w.it[k].tiles(w.it[k].count - 1));
+  }
+  w.pairs = __reduce_add_sync(0xffffffffu, w.pairs);
+  w.most = __reduce_max_sync(0xffffffffu, w.most);
+}
+// Pair p of the list, by key tiles descending: its sequence and place there.
+__device__ __forceinline__ void find_pair(const WholeList& w, int p, int lane, int& seq, int& u) {
+  auto count = [&](int T) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < LPT_SEQS / 32; ++k) n += pairs_from(w.it[k], T);
+    return (int)__reduce_add_sync(0xffffffffu, n);
+  };
+  int lo = 1, hi = w.most;              // the largest T with more than p pairs of T tiles or more
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (count(mid) > p) lo = mid; else hi = mid - 1;
+  }
+  int left = p - count(lo + 1);
+#pragma unroll
+  for (int k = 0; k < LPT_SEQS / 32; ++k) {
+    const int more = pairs_from(w.it[k], lo + 1), here = pairs_from(w.it[k], lo) - more;
+    int incl = here;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += x;
     }
-    const SeqInfo s = seq_info(P, lo, err);
-    const int u = pr - (s.q0 / per + lo);
+    const uint32_t found = __ballot_sync(0xffffffffu, left >= incl - here && left < incl);
+    if (found != 0) {
+      const int from = __ffs(found) - 1;
+      seq = from + 32 * k;
+      u = __shfl_sync(0xffffffffu, w.it[k].count - more - here + left - (incl - here), from);
+      left = NO_TILE;                   // in no later run
+    }
+    const int all = __shfl_sync(0xffffffffu, incl, 31);
+    if (left != NO_TILE) left -= all;
+  }
+}
+__device__ __forceinline__ void next_item(const SeqProb& P, WholeList& w, Seg& g, WsHeader* hdr, int lane) {
+  const int per = 2 * P.TQ;
+  while (true) {
+    unsigned item = blockIdx.x;
+    if (w.round > 0) {
+      if (lane == 0) item = gridDim.x + atomicAdd(&hdr->ticket, 1u);
+      item = __shfl_sync(0xffffffffu, item, 0);
+    }
+    ++w.round;
+    g.stop = item >= (P.n_seqs > LPT_SEQS ? P.items : (long long)w.pairs * P.Hkv);
+    if (g.stop) return;
+    const int pr = item / (unsigned)P.Hkv;
+    g.kvh = item - pr * P.Hkv;
+    int seq = 0, u;
+    if (P.n_seqs > LPT_SEQS) {
+      // sequence i's pairs lie at cu_q[i] / per + i and on (never more than
+      // the gap to the next sequence's first)
+      const int back = (int)(P.items / P.Hkv) - 1 - pr;
+      int hi = P.n_seqs - 1;
+      while (seq < hi) {
+        const int mid = (seq + hi + 1) >> 1;
+        if (P.cu_q[mid] / per + mid <= back) seq = mid; else hi = mid - 1;
+      }
+      u = back - (P.cu_q[seq] / per + seq);
+    } else {
+      find_pair(w, pr, lane, seq, u);
+    }
+    const SeqInfo s = seq_info(P, seq, &hdr->err);
     if (u < 0 || u >= ceil_div(s.Lq, per)) continue;
     g.lead = 0;
     g.row = s.row;
@@ -228,7 +300,6 @@ __device__ __forceinline__ void next_item(const SeqProb& P, Rounds& w, Seg& g, D
     fill_counts(P, g, 0, 1 << 30);
     return;
   }
-  g.stop = 1;
 }
 
 // Split keys: the next part of this CTA's share.
@@ -568,7 +639,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ segment list
-    Rounds rounds{0, 0};
+    WholeList whole;
+    if (!P.split) start_list(P, whole, lane, err);
+    const int ahead = P.split ? SEGS : 2;   // whole items: no further than needed, others may come to them first
     ShareWalk<KIND_MANY> w;
     if (P.split) {
       start_walk(P, mi->plan, w);
@@ -578,12 +651,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int ring = 0, q0 = 0, q1 = 0;
     Seg g;
     for (int k = 0;; ++k) {
+      if (k >= ahead && !wait_all(B_SEGEMPTY + (k - ahead) % SEGS, ((k - ahead) / SEGS) & 1, 0x4201)) break;
       if (P.split) next_part(P, mi->plan, w, g, err);
-      else next_item(P, rounds, g, err);
+      else next_item(P, whole, g, hdr, lane);
       g.ring = ring;
       g.qidx[0] = q0;
       g.qidx[1] = q1;
-      if (k >= SEGS && !wait_all(B_SEGEMPTY + k % SEGS, (k / SEGS - 1) & 1, 0x4201)) break;
       if (lane == 0) {
         mi->seg[k % SEGS] = g;
         mi->nf_tile[k % SEGS] = NO_TILE;
@@ -595,6 +668,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       ring += g.nload;
       q0 += g.n[0] > 0;
       q1 += g.n[1] > 0;
+    }
+    if (!P.split && lane == 0) {   // no CTA takes a ticket after its last: the last one out sets them back
+      __threadfence();
+      if (atomicAdd(&hdr->leaving, 1u) == gridDim.x - 1) {
+        hdr->ticket = 0;
+        hdr->leaving = 0;
+      }
     }
   } else if (warp == 11) {
     // ------------------------------------------------------------ copies

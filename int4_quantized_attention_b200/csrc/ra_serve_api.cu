@@ -116,6 +116,10 @@ ra_status sm_count(int* out) {
 constexpr int SM_BOUND = 148;
 
 // ---------------------------------------------------------------- packed
+// Upper bound of the work items of a packed call, from what the host knows.
+long long packed_items(int total_q, int n_seqs, int TQ, int Hkv) {
+  return ((long long)total_q / (2 * TQ) + n_seqs) * Hkv;
+}
 ra_status check_packed(const ra_packed* p) {
   if (p == nullptr) return fail(RA_ERR_INVALID_ARG, "problem is NULL");
   ra_status st = check_heads(p->Hq, p->Hkv, p->d);
@@ -126,6 +130,8 @@ ra_status check_packed(const ra_packed* p) {
   if (p->total_q < 0 || p->total_k < 0) return fail(RA_ERR_INVALID_ARG, "negative token count");
   if (p->total_q > (1 << 30) || p->total_k > (1 << 30) || p->n_seqs > (1 << 24))
     return fail(RA_ERR_UNSUPPORTED, "at most 2^30 tokens and 2^24 sequences");
+  if (packed_items(p->total_q, p->n_seqs, 128 / (p->Hq / p->Hkv), p->Hkv) >= (1ll << 31))
+    return fail(RA_ERR_UNSUPPORTED, "2^31 work items or more");
   if ((st = check_scale(p->scale)) != RA_OK) return st;
   if ((st = check_strides("q", p->q_token, p->q_head, p->total_q, p->Hq)) != RA_OK) return st;
   if ((st = check_strides("k", p->k_token, p->k_head, p->total_k, p->Hkv)) != RA_OK) return st;
@@ -133,10 +139,6 @@ ra_status check_packed(const ra_packed* p) {
   return check_out_strides(p->o_token, p->o_head, p->total_q, p->Hq);
 }
 
-// Upper bound of the work items of a packed call, from what the host knows.
-long long packed_items(int total_q, int n_seqs, int TQ, int Hkv) {
-  return ((long long)total_q / (2 * TQ) + n_seqs) * Hkv;
-}
 // Few items leave SMs idle: split the keys instead.
 bool packed_split(const ra_packed* p) {
   return packed_items(p->total_q, p->n_seqs, 128 / (p->Hq / p->Hkv), p->Hkv) < 2 * SM_BOUND;

@@ -80,6 +80,20 @@ def test_many_sequences(op):
     run_case(op, lens, lens, 4, 2, BF16, True)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n", [31, 32, 33, 128, 129])
+def test_item_order(op, n, causal):
+    # whole items, longest first, with as many sequences as one, several and too many rounds of lanes hold
+    lens = [(i * i * 37) % 400 + (700 if i % 13 == 5 else 0) for i in range(n)]
+    past = [(i % 4) * 61 for i in range(n)]
+    hq = 12 if n > 100 else 48
+    p = api.Packed(n, hq, hq, 128, 0, 0, sum(lens), sum(lens) + sum(past), 0.0, *([hq * 128, 128] * 4))
+    assert api.packed_workspace_bytes(p) == 256
+    out = run_case(op, lens, [a + b for a, b in zip(lens, past)], hq, hq, F16, causal)
+    for _ in range(3):                                   # tickets are set back each time
+        assert torch.equal(op.forward(*out[:3], ints(out[3]), ints(out[4]), causal=causal), out[5])
+
+
 def test_long_keys_few_rows(op):
     run_case(op, [3], [70001], 8, 1, F16, True)
 
