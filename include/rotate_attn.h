@@ -290,7 +290,8 @@ typedef enum { RA_FP16 = 0, RA_BF16 = 1 } ra_dtype;
  * sees no key gets zeros and a log-sum-exp of -infinity; rows behind
  * cu_q[n_seqs] are left as they were.  Keys and values that a token does not
  * see do not reach it, whatever they hold.
- * There is no position encoding: queries and keys come encoded. */
+ * There is no position encoding: queries and keys come encoded.  o and lse
+ * overlap no input. */
 typedef struct {
     int n_seqs;                 /* >= 1 */
     int Hq, Hkv, d;             /* Hq a multiple of Hkv, Hq / Hkv <= 128; d == 128 */
@@ -413,10 +414,12 @@ size_t ra_cache_attention_workspace_bytes(const ra_cache_problem *p, const ra_ca
  * tokens [cu_q[i], cu_q[i+1]) (cu_q NULL: token i), the last ones of its
  * lens[seqs[i]] tokens, written before the call; each sees the tokens up to
  * itself.  Rows may be named more than once.
- * The first `shared` tokens are read once for the whole batch, from the
- * longest sequence's pages: every sequence must hold the same pages there
- * (fork makes them so) as far as it reaches.  o, lse, workspace, errors: as in
- * ra_packed_attention_fwd.  Two launches. */
+ * The first `shared` tokens are read once for the whole batch, from the pages
+ * of one of its longest sequences: every sequence must hold the same pages
+ * there (fork makes them so) as far as it reaches.  Sequences of at most 64
+ * query rows (tokens x Hq / Hkv) run on one kernel, longer ones and the shared
+ * part on another; a third joins what was split.  o, lse, workspace, errors:
+ * as in ra_packed_attention_fwd. */
 ra_status ra_cache_attention_fwd(const ra_cache_problem *p, const ra_cache *c, const ra_cache_attn *a, const void *q,
                                  const int *seqs, const int *cu_q, void *o, float *lse, void *workspace,
                                  size_t workspace_bytes, ra_stream stream);

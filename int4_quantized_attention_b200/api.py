@@ -437,6 +437,8 @@ class _Workspace:
 
     def grow(self, need: int):
         import torch
+        if torch.cuda.is_current_stream_capturing():   # its zeroing would wait for the first replay
+            raise _bad("workspace", "make the first call of this size before capturing it")
         size = max(need, 2 * self.buffers[-1].numel()) if self.buffers else need
         self.buffers.append(torch.zeros((size,), dtype=torch.uint8, device=self.device))
         return self.buffers[-1]

@@ -402,7 +402,7 @@ ra_status ra_cache_write(const ra_cache_problem* p, const ra_cache* c, int layer
   if (!aligned(k, 16) || !aligned(v, 16)) return fail(RA_ERR_INVALID_ARG, "k or v NULL or not 16-byte aligned");
   if ((st = check_strides("k", k_token, k_head, total, p->Hkv)) != RA_OK) return st;
   if ((st = check_strides("v", v_token, v_head, total, p->Hkv)) != RA_OK) return st;
-  if ((long long)total * p->Hkv >= (1ll << 34)) return fail(RA_ERR_UNSUPPORTED, "too many rows for one call");
+  if ((long long)total * p->Hkv >= (1ll << 33)) return fail(RA_ERR_UNSUPPORTED, "too many rows for one call");
   const cudaError_t e = ra::launch_cache_write(C, layer, seqs, cu_new, n, total, static_cast<const uint8_t*>(k),
                                                static_cast<const uint8_t*>(v), 2 * k_token, 2 * k_head, 2 * v_token,
                                                2 * v_head, ws, static_cast<cudaStream_t>(stream));

@@ -351,6 +351,87 @@ def test_prompt_over_the_cache():
     run_attention(c, m, [0, 1, 2], [300, 129, 1], 8, 64)
 
 
+def test_more_query_tokens_than_the_row_holds():
+    c, m = filled([3, 70, 2], 0, 16, 2, F16, seed=20)
+    q, cu, o = run_attention(c, m, [0, 1, 2], [5, 70, 90], 4, 0)
+    assert bool((o[:2] == 0).all()) and bool((o[75:75 + 88] == 0).all())
+
+
+@pytest.mark.parametrize("shared", [0, 256])
+def test_many_heads_per_key_head(shared):
+    # more rows per token than the kernel of few rows takes
+    c, m = filled([1, 130, 700], shared, 32, 1, BF16, seed=21)
+    run_attention(c, m, [0, 1, 2], [1, 1, 1], 128, shared)
+    run_attention(c, m, [0, 1, 2], [1, 3, 2], 72, shared)
+
+
+def test_rows_behind_the_last_sequence_stay():
+    for shared in (0, 64):
+        c, m = filled([30, 200], shared, 16, 2, F16, seed=22)
+        q = rand(3, 40, 4, D)
+        out = torch.full((40, 4, D), 3.0, device="cuda", dtype=F16)
+        lse = torch.full((40, 4), 5.0, device="cuda")
+        c.attention(0, q, ints([0, 1]), cu_q=ints([0, 2, 25]), shared=shared, out=out, lse=lse)
+        c.check()
+        assert bool((out[25:] == 3).all()) and bool((lse[25:] == 5).all())
+        want, wl, tol, tl = paged(c.pool, 0, m.rows, m.lens, q[:25], [0, 1], [0, 2, 25])
+        check(out[:25], want, tol, "o")
+        check(lse[:25], wl, tl, "lse")
+
+
+def test_every_row_shorter_than_the_shared_part():
+    c, m = filled([30, 60, 9], 128, 16, 1, F16, seed=23, nan_tail=False)
+    for i, n in enumerate((40, 100, 0)):
+        c.lens[i] = n
+        m.lens[i], m.rows[i] = n, m.rows[i][:-(-n // 16)]
+    run_attention(c, m, [0, 1, 2], [1, 1, 1], 2, 128)
+    run_attention(c, m, [2, 0, 1], [1, 40, 3], 2, 128)
+
+
+def test_strided_queries_and_outputs():
+    c, m = filled([30, 200, 5], 32, 16, 2, BF16, seed=24)
+    big = rand(3, 3, 10, D, dtype=BF16)
+    q = big[:, 1:9]                                     # heads 1 to 8 of 10
+    out = torch.full((3, 16, D), 3.0, device="cuda", dtype=BF16)[:, ::2]
+    got = c.attention(0, q, ints([0, 1, 2]), shared=32, out=out)
+    c.check()
+    want, _, tol, _ = paged(c.pool, 0, m.rows, m.lens, q, [0, 1, 2], [0, 1, 2, 3])
+    check(got, want, tol, "o")
+    headed = rand(3, 8, 3, D, dtype=BF16).transpose(0, 1)   # head-major
+    headed.copy_(q)
+    assert torch.equal(c.attention(0, headed, ints([0, 1, 2]), shared=32), out)
+
+
+def test_workspace_content_does_not_matter():
+    c, m = filled([30, 200, 700], 128, 16, 2, F16, seed=25)
+    q = rand(3, 8, 8, D)
+    cu = ints([0, 1, 7, 8])
+    want = c.attention(0, q, ints([0, 1, 2]), cu_q=cu, shared=128)
+    c._ws.current()[256:] = 0x77
+    c._work[256:] = 0x77
+    assert torch.equal(c.attention(0, q, ints([0, 1, 2]), cu_q=cu, shared=128), want)
+    c.extend(ints([1]), ints([40]))
+    m.extend([1], [40])
+    c.fork(ints([1, 0]), ints([3, -1]))
+    m.fork([1], [3])
+    c.free(ints([0]))
+    m.free([0])
+    c.compact()
+    m.compact()
+    m.same()
+
+
+def test_growing_while_capturing_is_refused():
+    c, m = filled([30], 0, 16, 2, F16, seed=26)
+    q, row = rand(3, 1, 4, D), ints([0])
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(api.RotateAttnError):
+        with torch.cuda.graph(graph):
+            c.attention(0, q, row)
+    torch.cuda.synchronize()
+    run_attention(c, m, [0], [1], 4, 0)
+
+
 def test_padded_and_repeated_rows():
     c, m = filled([30, 200], 32, 16, 2, F16, seed=10)
     q, cu, o = run_attention(c, m, [-1, 1, 0, 1, -1], [1] * 5, 4, 32)

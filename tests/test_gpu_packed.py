@@ -226,6 +226,27 @@ def test_repeatable_captured_and_on_a_side_stream(op):
     check(out, want, tol, "replayed")
 
 
+def test_two_streams_at_once():
+    # calls of two objects may overlap: each has its own workspace
+    cases = [([900, 31], 8, 2, BF16), ([500, 700, 300, 2], 40, 40, F16)]
+    sets = []
+    for lens, hq, hkv, dtype in cases:
+        cu = cum(lens)
+        q, k, v = inputs(7, cu[-1], cu[-1], hq, hkv, dtype)
+        sets.append((api.PackedAttention(), torch.cuda.Stream(), q, k, v, ints(cu), packed(q, k, v, cu, cu, True)))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for i, (mine, stream, q, k, v, cu, _) in enumerate(sets):
+            with torch.cuda.stream(stream):
+                outs[i].append(mine.forward(q, k, v, cu, cu))
+    torch.cuda.synchronize()
+    for i, (mine, _, _, _, _, _, (want, _, tol, _)) in enumerate(sets):
+        mine.check()
+        check(outs[i][0], want, tol, "o")
+        assert all(torch.equal(x, outs[i][0]) for x in outs[i])
+
+
 def test_bad_offsets_are_reported_and_left_out(op):
     q, k, v = inputs(2, 100, 100, 2, 2, F16)
     for cq, ck, fine in (([0, 40, 30], [0, 40, 100], 40), ([0, 40, 101], [0, 40, 100], 40),
