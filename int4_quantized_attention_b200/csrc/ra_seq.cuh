@@ -134,7 +134,7 @@ template <int KIND>
 struct Kind;
 template <>
 struct Kind<KIND_MANY> {
-  static constexpr int TILE = KEYS, W_ITEM = 128, SLOT = SLOT_ROWS;
+  static constexpr int TILE = KEYS, W_ITEM = 384, SLOT = SLOT_ROWS;
   __device__ static __forceinline__ int tokens_per_item(const SeqProb& P) { return 2 * P.TQ; }
 };
 template <>
@@ -195,7 +195,7 @@ __device__ __forceinline__ int quotient(long long a, long long b) {
 // item's first and last holds one of its tiles.
 __device__ __forceinline__ long long share_of(long long total, int ctas) {
   const long long t = total + ctas - 1;
-  return max(t >> 32 == 0 ? (long long)((uint32_t)t / (uint32_t)ctas) : t / ctas, 320ll);
+  return max(t >> 32 == 0 ? (long long)((uint32_t)t / (uint32_t)ctas) : t / ctas, 200ll);
 }
 
 // In shared memory: the plan of one CTA.
