@@ -20,7 +20,14 @@
 // 16 at a time, with a running maximum, sum and fp32 accumulator of its own; the
 // 4 / R partial results of each row are joined through shared memory at the
 // end of the part.  The work is dealt as in the split form of ra_packed.cu:
-// equal shares of all tiles, parts of an item joined by the combine kernel.
+// equal shares of all keys, parts of an item put together by the joining kernel.
+//
+// What it measured: 24 sequences of 8000 tokens, 40/8 heads (787 MB): 126 us,
+// 6.22 TB/s, 0.95 of the measured copy.  On the 128-row tiles the same call took
+// 160 us, and 48 sequences of 1 to 16384 tokens 228 us where it takes 90: short
+// parts cost a pipeline of one CTA per SM its full latency each time.  A part
+// costs some 9,000 cycles besides its tiles (3,800 each, three CTAs sharing the
+// memory), which W_ITEM charges it for.
 #include "ra_seq.cuh"
 
 namespace ra {

@@ -11,29 +11,39 @@
 // Work item: a pair of 128-row query tiles A, B of one key head.  Row r of a
 // tile is token r / G, query head r % G of the group, so that the G heads
 // that share a key head share its K and V tiles, short prompts fill rows with
-// heads, and a single token's G rows need one pass over its keys.
+// heads, and a token's G rows need one pass over its keys.
 //
-// Every CTA is persistent (one per SM) and walks a list of segments: (item,
+// Every CTA is persistent (one per SM) and works through segments: (item,
 // range of 128-key tiles).  Two ways to deal them out:
-//   whole items  one at a time to the CTA that is free, long ones first.  Rows
-//                are final.
-//   split        all key tiles of all items, laid end to end, are cut into
-//                equal shares, one per CTA, whatever the lengths are; an item
-//                that crosses a border leaves partial rows (fp32) that
-//                the joining kernel puts together.  For few rows over many keys, and
-//                wherever there is a shared region.
+//   whole items  one at a time to the CTA that is free, those with the most key
+//                tiles first.  Rows are final.
+//   split        all items, laid end to end, are cut into equal shares, one per
+//                CTA, whatever the lengths are; an item that crosses a border
+//                leaves partial rows (fp32) that a joining kernel puts together.
+//                For few items (below two per SM), and wherever there is a shared
+//                region.  With more, whole items win, since a share's first and
+//                last rows go through memory once more: 13 prompts of 40 to 2048
+//                tokens, 32/8 heads, 149 us against 224; one of 4096, 24 heads, both
+//                ways, 215 against 227.
 //
-// 384 threads, the pipeline of the FP16 fallback kernel:
+// 384 threads:
 //   warps 0-3 / 4-7   softmax of tile A / B; thread t = row t = TMEM lane t
-//   warp 8            segment list, Q and K copies
-//   warp 11           V copies
+//   warp 8            the segment list, a few segments ahead
 //   warps 9, 10       MMA issuers of tile A / B (warp 9 owns TMEM)
+//   warp 11           copies
 // Copies are TMA tiles straight from the caller's tensors (any token and head
 // strides), 64 channels wide with the 128-byte swizzle; a 128-key tile of a
-// cache is one box per page and half.  V keeps its [key][channel] order and
-// is the P.V product's N-major B operand, so nothing is transposed.
+// cache is one box per page and half, one per lane.  V keeps its [key][channel]
+// order and is the P.V product's N-major B operand, so nothing is transposed.
+// K and V have two stages of 32 KB each.
 // TMEM: S_A | S_B | O_A | O_B, 128 fp32 columns each; P overwrites the upper
 // half of S as 16-bit pairs and is the A operand of the P.V product.
+//
+// What bounds it: from some thousand tokens on the power limit (8192 and more
+// tokens run at 1.55 to 1.7 GHz and 990 W: 1040 to 1100 TFLOP/s, of 1377 that a
+// bf16 matrix product sustains there); below, what a segment costs besides its
+// tiles (a masked tile's softmax 3500 to 6000 cycles against 3340 per pair of
+// tiles in the middle of a sequence, the epilogue 4000).
 //
 // Precision: S, the row statistics, O and partial rows are fp32.  P is
 // rounded to the type of V (the tensor core wants both operands alike):
@@ -77,6 +87,7 @@ enum : int {
   B_KFULL = 0, B_KEMPTY = 2, B_VFULL = 4, B_VEMPTY = 6, B_QFULL = 8, B_QEMPTY = 10, B_SFULL = 12, B_PFULL = 14,
   B_ODONE = 18, B_DRAIN = 20, B_TURN = 22, B_SEGFULL = 24, B_SEGEMPTY = 32, NBAR = 40
 };
+
 // A segment, as the list warp publishes it.
 struct Seg {
   int stop;
