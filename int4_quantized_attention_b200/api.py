@@ -464,7 +464,6 @@ class PackedAttention:
         """q [total_q, Hq, 128], k and v [total_k, Hkv, 128], fp16 or bf16, any
         token and head strides that are multiples of 8 elements; cu_q and cu_k
         int32 [n + 1] on the device.  Returns out, or (out, lse)."""
-        import torch
         call = "packed_attention"
         dtype = q.dtype
         code = _dtype(call, dtype)
@@ -475,10 +474,10 @@ class PackedAttention:
         _ints(call, "cu_k", cu_k, self.device, cu_q.numel())
         total_q, Hq = q.shape[0], q.shape[1]
         if out is None:
-            out = torch.empty((total_q, Hq, 128), dtype=dtype, device=self.device)
+            out = q.new_empty(q.shape)
         else:
             _rows(call, "out", out, dtype, self.device, Hq, total_q)
-        lse = _lse(call, lse, return_lse, total_q, Hq, self.device)
+        lse = _lse(call, lse, return_lse, q)
         p = Packed(cu_q.numel() - 1, Hq, k.shape[1], 128, code, int(bool(causal)), total_q, k.shape[0], scale,
                    q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
                    out.stride(0), out.stride(1))
@@ -521,12 +520,13 @@ class _on:
             torch.cuda.set_device(self.before)
 
 
-def _lse(call: str, lse, wanted: bool, tokens: int, heads: int, device):
+def _lse(call: str, lse, wanted: bool, q):
     import torch
+    rows = q.shape[:2]
     if lse is None:
-        return torch.empty((tokens, heads), dtype=torch.float32, device=device) if wanted else None
-    if lse.shape != (tokens, heads) or lse.dtype != torch.float32 or lse.device != device or not lse.is_contiguous():
-        raise _bad(call, f"lse: a contiguous float32 [{tokens}, {heads}] tensor on {device}")
+        return q.new_empty(rows, dtype=torch.float32) if wanted else None
+    if lse.shape != rows or lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous():
+        raise _bad(call, f"lse: a contiguous float32 {list(rows)} tensor on {q.device}")
     return lse
 
 
@@ -612,7 +612,6 @@ class PagedCache:
         """The newest tokens q [total_q, Hq, 128] of rows `seqs` (token i, or
         tokens cu_q[i] to cu_q[i + 1] of row i) over their sequences, whose
         first `shared` tokens lie in the same pages.  Returns out, or (out, lse)."""
-        import torch
         call = "cache_attention"
         _rows(call, "q", q, self.dtype, self.device)
         _ints(call, "seqs", seqs, self.device)
@@ -620,10 +619,10 @@ class PagedCache:
             _ints(call, "cu_q", cu_q, self.device, seqs.numel() + 1)
         total_q, Hq = q.shape[0], q.shape[1]
         if out is None:
-            out = torch.empty((total_q, Hq, 128), dtype=self.dtype, device=self.device)
+            out = q.new_empty(q.shape)
         else:
             _rows(call, "out", out, self.dtype, self.device, Hq, total_q)
-        lse = _lse(call, lse, return_lse, total_q, Hq, self.device)
+        lse = _lse(call, lse, return_lse, q)
         a = CacheAttn(seqs.numel(), Hq, total_q, layer, shared, scale, q.stride(0), q.stride(1), out.stride(0),
                       out.stride(1))
         ref = ctypes.byref(a)
