@@ -100,8 +100,11 @@ __global__ void __launch_bounds__(THREADS, FEW_CTAS) few_kernel(const __grid_con
     auto copy_tile = [&](int t, int stage) {
       const uint32_t k_dst = ring + stage * 2 * HALF_STAGE, v_dst = k_dst + HALF_STAGE;
       int page = -1, slot = -1;
+      // past the part's end nothing is copied: not even zeros, which would land
+      // on the rows that faster warps already lay out for the join
 #pragma unroll
       for (int i = 0; i < FEW_KEYS / 8; ++i) {
+        if (t == NO_COPY) break;
         const int r = copy_row + 8 * i, key = t * FEW_KEYS + r, pos = key0 + key;
         bool there = key < len;
         if (there && (pos >> P.page_shift) != slot) {

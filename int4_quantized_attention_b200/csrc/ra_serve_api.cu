@@ -94,7 +94,8 @@ ra_status check_out_strides(long long tok, long long head, long long tokens, int
 cuuint64_t map_stride(long long s, long long n) { return n <= 1 ? 256 : (cuuint64_t)s * 2; }
 
 ra_status check_scale(double scale) {
-  if (!(scale >= 0.0) || !std::isfinite((float)(scale * 1.4426950408889634)))
+  const float c = (float)(scale * 1.4426950408889634);   // what the kernels multiply scores by
+  if (!(scale >= 0.0) || !std::isfinite(c) || (scale > 0.0 && c == 0.0f))
     return fail(RA_ERR_INVALID_ARG, "softmax scale must be positive and finite (0: 1/sqrt(d))");
   return RA_OK;
 }

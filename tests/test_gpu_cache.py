@@ -351,6 +351,18 @@ def test_prompt_over_the_cache():
     run_attention(c, m, [0, 1, 2], [300, 129, 1], 8, 64)
 
 
+def test_same_result_every_time():
+    # many full 64-row parts: what one warp still copies or reads must not meet what another lays out
+    rng = random.Random(1)
+    lens = [rng.randint(1, 3000) for _ in range(90)]
+    counts = [rng.choice([0, 1, 1, 2, 5, min(n + 3, 70)]) for n in lens]
+    for hq, dtype in ((64, F16), (24, BF16)):
+        c, m = filled(lens, 0, 128, 1, dtype, seed=5)
+        q, cu, o = run_attention(c, m, list(range(90)), counts, hq, 0)
+        for _ in range(30):
+            assert torch.equal(c.attention(0, q, ints(list(range(90))), cu_q=ints(cu)), o)
+
+
 def test_more_query_tokens_than_the_row_holds():
     c, m = filled([3, 70, 2], 0, 16, 2, F16, seed=20)
     q, cu, o = run_attention(c, m, [0, 1, 2], [5, 70, 90], 4, 0)

@@ -34,6 +34,8 @@ def call_packed(lib, p, q=A, k=A, v=A, cq=A, ck=A, o=A, lse=None, ws=A, size=1 <
     (dict(n_seqs=0), api.RA_ERR_INVALID_ARG), (dict(dtype=2), api.RA_ERR_INVALID_ARG),
     (dict(causal=2), api.RA_ERR_INVALID_ARG), (dict(total_q=-1), api.RA_ERR_INVALID_ARG),
     (dict(total_k=1 << 30 | 1), api.RA_ERR_UNSUPPORTED), (dict(scale=-1.0), api.RA_ERR_INVALID_ARG),
+    (dict(scale=1e-60), api.RA_ERR_INVALID_ARG), (dict(total_q=1 << 29, Hq=4096, Hkv=4096, q_token=4096 * 128,
+                                                       o_token=4096 * 128), api.RA_ERR_UNSUPPORTED),
     (dict(scale=float("nan")), api.RA_ERR_INVALID_ARG), (dict(scale=float("inf")), api.RA_ERR_INVALID_ARG),
     (dict(q_token=1020), api.RA_ERR_INVALID_ARG), (dict(k_head=0), api.RA_ERR_INVALID_ARG),
     (dict(v_token=0), api.RA_ERR_INVALID_ARG), (dict(o_token=512), api.RA_ERR_INVALID_ARG),
