@@ -116,9 +116,7 @@ __host__ Ws ws_of(const CacheProb& c, void* ws) {
 
 __device__ __forceinline__ int pages_for(const CacheProb& c, int len) { return (len + c.page_size - 1) >> c.page_shift; }
 __device__ __forceinline__ bool row_ok(const CacheProb& c, int row) {
-  if (row < 0 || row >= c.max_seqs) return false;
-  const int len = c.lens[row];
-  return len >= 0 && (long long)len <= (long long)c.max_pages << c.page_shift;
+  return row >= 0 && row < c.max_seqs && row_fits(c.lens[row], c.max_pages, c.page_shift);
 }
 
 enum : int { BAD = 1, TOO_MUCH = 2 };   // flags of a scan

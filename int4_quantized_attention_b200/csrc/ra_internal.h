@@ -60,6 +60,12 @@ struct WsLayout {
   size_t total_fp16;
 };
 
+// Whether a row of `len` tokens fits a table row of max_pages pages.  max_pages
+// << page_shift is below 2^30; len may be any int, so nothing is added to it.
+__host__ __device__ __forceinline__ bool row_fits(int len, int max_pages, int page_shift) {
+  return len >= 0 && len <= max_pages << page_shift;
+}
+
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 inline WsLayout ws_layout(const Prob& p) {

@@ -45,7 +45,7 @@ __device__ __forceinline__ SeqInfo seq_info(const SeqProb& P, int i, DeviceErr* 
     const int r = P.seqs[i];
     if (r >= 0 && r < P.max_seqs) {
       const int L = P.lens[r];
-      if (L >= 0 && (L + P.page_size - 1) >> P.page_shift <= P.max_pages) {
+      if (row_fits(L, P.max_pages, P.page_shift)) {
         s.row = r;
         s.L = L;
       } else {

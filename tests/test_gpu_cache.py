@@ -528,6 +528,28 @@ def test_bad_pages_are_reported():
     c.check()
 
 
+@pytest.mark.parametrize("shared", [0, 32])
+def test_lengths_near_the_largest_int_are_reported(shared):
+    # a length that no table row holds leaves the sequence out, also where one page more passes 2^31
+    c, m = filled([100, 50], shared, 16, 1, F16, seed=15)
+    q = rand(3, 2, 1, D)
+    want, wl, tol, tl = paged(c.pool, 0, m.rows, m.lens, q, [-1, 1], [0, 1, 2])
+    for bad in (2 ** 31 - 1, 2 ** 31 - 14, 2 ** 31 - 16, 2 ** 30, c.p.max_pages * 16 + 1, -1, -2 ** 31):
+        c.lens[0] = bad
+        for cu in (None, ints([0, 1, 2])):
+            o, lse = c.attention(0, q, ints([0, 1]), cu_q=cu, shared=shared, return_lse=True)
+            with pytest.raises(api.RotateAttnError) as e:
+                c.check()
+            assert e.value.status == api.RA_ERR_DEVICE_BOUNDS
+            check(o, want, tol, "o")                    # row 0: zeros, -inf
+            check(lse, wl, tl, "lse")
+        before = c.state.clone()
+        c.free(ints([0]))
+        with pytest.raises(api.RotateAttnError):
+            c.check()
+        assert torch.equal(c.state, before)
+
+
 def test_a_pool_past_32_bit_offsets():
     # the last pages of a 9 GB pool: element offsets pass 2^32
     n = 1 << 16
