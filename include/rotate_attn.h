@@ -376,7 +376,11 @@ ra_status ra_cache_extend(const ra_cache_problem *p, const ra_cache *c, const in
 /* Writes the last tokens of each row in one layer: row seqs[i] gets tokens
  * [cu_new[i], cu_new[i+1]) of k and v (cu_new NULL: token i), at positions
  * lens - count and on.  k, v: [total][Hkv][128] with the given strides
- * (elements; multiples of 8).  A row is named once at most. */
+ * (elements; multiples of 8).  cu_new: int32 [n + 1], ascending within 0 ..
+ * total; tokens outside it are passed over.  Nothing is written, and
+ * RA_ERR_DEVICE_BOUNDS reported, also where cu_new descends or leaves that
+ * range, a row is shorter than its tokens, or the table names no page for one.
+ * One launch for short lists, two otherwise. */
 ra_status ra_cache_write(const ra_cache_problem *p, const ra_cache *c, int layer, const int *seqs, const int *cu_new,
                          int n, int total, const void *k, const void *v, long long k_token, long long k_head,
                          long long v_token, long long v_head, void *workspace, size_t workspace_bytes,

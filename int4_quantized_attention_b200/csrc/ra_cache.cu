@@ -23,6 +23,7 @@
 #include <cstdint>
 
 #include "ra_cache.h"
+#include "ra_launch.cuh"
 
 namespace ra {
 namespace {
@@ -31,6 +32,7 @@ constexpr int CL = 8;              // CTAs of the state cluster
 constexpr int CT = 1024;           // threads per CTA of it
 constexpr int ALL = CL * CT;
 constexpr int COPY_CTAS = 8 * 148;   // 2048 threads per SM
+constexpr int WRITE_CT = 256;      // threads per CTA of a write
 
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -370,38 +372,144 @@ __global__ void __launch_bounds__(256) copy_kernel(CacheProb c, Ws w, int remap)
   }
 }
 
+// ---------------------------------------------------------------- write
+// A write is checked as a whole before any of it is stored.  The checks need
+// one thread for each entry of the list and for each page that the tokens lie
+// in; `at` of `all` threads call this.  Rows named twice are found elsewhere.
+// Returns BAD or 0, by thread.
+__device__ int check_write(const CacheProb& c, const int* seqs, const int* cu_new, int n, int total, int at, int all) {
+  int bad = 0;
+  auto entry = [&](int i, int& row, int& count) {   // false: nothing of it is written
+    row = seqs[i];
+    count = 1;
+    if (cu_new != nullptr) {
+      const int a = cu_new[i], b = cu_new[i + 1];
+      if (a < 0 || b < a || b > total) {
+        bad = BAD;
+        return false;
+      }
+      count = b - a;
+    }
+    if (row == -1) return false;
+    if (!row_ok(c, row) || c.lens[row] < count) {
+      bad = BAD;
+      return false;
+    }
+    return count > 0;
+  };
+  // entry i has floor(cu_new[i] / page_size) + 2 i as its first page's number:
+  // count tokens lie in at most floor(count / page_size) + 2 pages
+  const long long pages = cu_new == nullptr ? n : (total >> c.page_shift) + 2ll * n;
+  for (long long u = at; u < pages; u += all) {
+    int i = (int)u, j = 0, row, count;
+    if (cu_new != nullptr) {
+      auto first = [&](int e) { return (cu_new[e] >> c.page_shift) + 2ll * e; };
+      int lo = 0, hi = n - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first(mid) <= u) lo = mid; else hi = mid - 1;
+      }
+      i = lo;
+      const long long past = u - first(i);
+      if (past < 0) continue;
+      j = (int)min(past, 1ll << 30);
+    }
+    if (!entry(i, row, count)) continue;
+    const int len = c.lens[row], slot = ((len - count) >> c.page_shift) + j;
+    if (slot > (len - 1) >> c.page_shift) continue;
+    const int page = c.table[(long long)row * c.max_pages + slot];
+    if ((uint32_t)page >= (uint32_t)c.n_pages) bad = BAD;
+  }
+  if (cu_new != nullptr) {   // entries without tokens or with bad offsets have no page of their own above
+    int row, count;
+    for (int i = at; i < n; i += all) entry(i, row, count);
+  }
+  return bad;
+}
+
+// Long lists and many tokens: one cluster checks, the copy waits for its word.
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
+    write_check_kernel(CacheProb c, const int* __restrict__ seqs, const int* __restrict__ cu_new, int n, int total, Ws w) {
+  __shared__ Shared sh;
+  dependents_may_start();
+  const int at = ctarank() * CT + threadIdx.x;
+  const int flags = check_rows(c, w, seqs, n, nullptr) | check_write(c, seqs, cu_new, n, total, at, ALL);
+  const bool no = refused(cluster_scan(0, 0, flags, &sh), w.hdr, 0x5041);
+  if (at == 0) w.jobs[1] = !no;
+}
+
 // New tokens into their slots: 16 lanes per (token, head, keys or values).
-__global__ void __launch_bounds__(256)
+// CHECKED: write_check_kernel's word decides, and the copies wait for it with
+// their data in hand.  Otherwise the list is short, and a second half of every
+// CTA checks all of it meanwhile (short_write says when): a launch more costs
+// small writes what they take altogether.
+template <bool CHECKED>
+__global__ void __launch_bounds__(CHECKED ? WRITE_CT : 2 * WRITE_CT)
     write_kernel(CacheProb c, int layer, const int* __restrict__ seqs, const int* __restrict__ cu_new, int n, int total,
                  const uint8_t* __restrict__ k, const uint8_t* __restrict__ v, long long k_tok, long long k_head,
-                 long long v_tok, long long v_head, WsHeader* hdr) {
-  const int lane16 = threadIdx.x & 15;
-  const long long unit = ((long long)blockIdx.x * 256 + threadIdx.x) >> 4;
-  const int per = 2 * c.Hkv;
-  if (unit >= (long long)total * per) return;
-  const int t = (int)(unit / per), part = (int)(unit % per), head = part % c.Hkv;
-  const bool is_v = part >= c.Hkv;
-  int i = t, first = t, count = 1;
-  if (cu_new != nullptr) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (cu_new[mid] <= t) lo = mid; else hi = mid - 1;
+                 long long v_tok, long long v_head, Ws w) {
+  __shared__ int rows[CHECKED ? 1 : WRITE_CT];
+  int bad = 0;
+  uint4 x = make_uint4(0, 0, 0, 0);
+  uint4* dst = nullptr;
+  if (!CHECKED && threadIdx.x >= WRITE_CT) {
+    const int me = threadIdx.x - WRITE_CT, row = me < n ? seqs[me] : -1;
+    rows[me] = row;
+    bad = check_write(c, seqs, cu_new, n, total, me, WRITE_CT);
+    asm volatile("bar.sync 1, %0;" ::"n"(WRITE_CT) : "memory");
+    if (row != -1) {
+#pragma unroll 8
+      for (int j = 0; j < n; ++j)
+        if (j != me && rows[j] == row) bad = BAD;
     }
-    i = lo;
-    first = cu_new[i];
-    count = cu_new[i + 1] - first;
-    if (t < first || t >= first + count) return;   // behind the last sequence
+  } else {
+    // this thread's piece and its slot; whatever a bad list names is passed over, the checks find it
+    const int lane16 = threadIdx.x & 15;
+    const long long unit = ((long long)blockIdx.x * WRITE_CT + threadIdx.x) >> 4;
+    const int per = 2 * c.Hkv;
+    if (unit < (long long)total * per) {
+      const int t = (int)(unit / per), part = (int)(unit % per), head = part % c.Hkv;
+      const bool is_v = part >= c.Hkv;
+      int i = t, first = t, last = t + 1;
+      if (cu_new != nullptr) {
+        int lo = 0, hi = n - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (cu_new[mid] <= t) lo = mid; else hi = mid - 1;
+        }
+        i = lo;
+        first = cu_new[i];
+        last = cu_new[i + 1];
+      }
+      const int row = seqs[i];
+      if (first >= 0 && t >= first && t < last && row != -1 && row_ok(c, row) && c.lens[row] >= last - first) {
+        const int pos = c.lens[row] - (last - t);
+        const int page = c.table[(long long)row * c.max_pages + (pos >> c.page_shift)];
+        if ((uint32_t)page < (uint32_t)c.n_pages) {
+          const long long slot = (((long long)layer * c.n_pages + page) * c.Hkv + head) * c.page_size + (pos & (c.page_size - 1));
+          x = reinterpret_cast<const uint4*>(is_v ? v + t * v_tok + head * v_head : k + t * k_tok + head * k_head)[lane16];
+          dst = reinterpret_cast<uint4*>((is_v ? c.v : c.k) + slot * 256) + lane16;
+        }
+      }
+    }
   }
-  const int row = seqs[i];
-  if (row == -1) return;
-  if (!row_ok(c, row) || c.lens[row] < count) return report(&hdr->err, DEVERR_BOUNDS, 0x5041);
-  const int pos = c.lens[row] - count + (t - first);
-  const int page = c.table[(long long)row * c.max_pages + (pos >> c.page_shift)];
-  if ((uint32_t)page >= (uint32_t)c.n_pages) return report(&hdr->err, DEVERR_BOUNDS, 0x5042);
-  const uint8_t* src = is_v ? v + t * v_tok + head * v_head : k + t * k_tok + head * k_head;
-  const long long slot = (((long long)layer * c.n_pages + page) * c.Hkv + head) * c.page_size + (pos & (c.page_size - 1));
-  reinterpret_cast<uint4*>((is_v ? c.v : c.k) + slot * 256)[lane16] = reinterpret_cast<const uint4*>(src)[lane16];
+  if constexpr (CHECKED) {
+    wait_for_predecessor();
+    if (w.jobs[1] == 0) return;
+  } else if (__syncthreads_or(bad)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) report(&w.hdr->err, DEVERR_BOUNDS, 0x5041);
+    return;
+  }
+  if (dst != nullptr) *dst = x;
+}
+
+// Each CTA checks the whole list itself while that is little work, which grows
+// with the list and with the CTAs (tokens x heads).  In every CTA / by a launch
+// of its own, 8 heads: 64 single tokens 3.2 / 6.1 us, 250 6.1 / 6.6, 64 x 8
+// tokens 5.5 / 7.1, 64 x 16 9.0 / 7.7, 250 x 3 19.7 / 7.9, one row of 1024 5.0 /
+// 7.4.  (Without any check: 2.2, 2.3, 3.7, 4.2, 4.2 and 3.4 us.)
+bool short_write(const CacheProb& c, int n, int total) {
+  return n <= WRITE_CT && total <= 4 * WRITE_CT && (long long)n * total * c.Hkv < 1 << 19;
 }
 
 cudaError_t launch_copy(const CacheProb& c, const Ws& w, int remap, cudaStream_t st) {
@@ -440,11 +548,19 @@ cudaError_t launch_cache_compact(const CacheProb& c, void* ws, cudaStream_t st) 
 cudaError_t launch_cache_write(const CacheProb& c, int layer, const int* seqs, const int* cu_new, int n, int total,
                                const uint8_t* k, const uint8_t* v, long long k_tok, long long k_head, long long v_tok,
                                long long v_head, void* ws, cudaStream_t st) {
-  const long long units = (long long)total * 2 * c.Hkv;
-  write_kernel<<<(unsigned)((units * 16 + 255) / 256), 256, 0, st>>>(c, layer, seqs, cu_new, n, total, k, v, k_tok,
-                                                                      k_head, v_tok, v_head,
-                                                                      static_cast<WsHeader*>(ws));
-  return cudaGetLastError();
+  const Ws w = ws_of(c, ws);
+  const long long threads = (long long)total * 2 * c.Hkv * 16;
+  const unsigned grid = (unsigned)((threads + WRITE_CT - 1) / WRITE_CT);
+  if (short_write(c, n, total)) {
+    write_kernel<false><<<grid > 0 ? grid : 1, 2 * WRITE_CT, 0, st>>>(c, layer, seqs, cu_new, n, total, k, v, k_tok, k_head,
+                                                                  v_tok, v_head, w);
+    return cudaGetLastError();
+  }
+  write_check_kernel<<<CL, CT, 0, st>>>(c, seqs, cu_new, n, total, w);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || grid == 0) return e;
+  return launch_after(true, write_kernel<true>, grid, WRITE_CT, 0, st, c, layer, seqs, cu_new, n, total, k, v, k_tok,
+                      k_head, v_tok, v_head, w);
 }
 
 }  // namespace ra

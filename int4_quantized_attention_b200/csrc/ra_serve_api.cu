@@ -401,9 +401,9 @@ ra_status ra_cache_write(const ra_cache_problem* p, const ra_cache* c, int layer
   if (total < 0 || (cu_new == nullptr && total != n) || (n == 0 && total > 0))
     return fail(RA_ERR_INVALID_ARG, "%d tokens for %d rows", total, n);
   if (cu_new != nullptr && !aligned(cu_new, 4)) return fail(RA_ERR_INVALID_ARG, "cu_new misaligned");
-  if (total == 0) return RA_OK;
+  if (n == 0) return RA_OK;
   if (total > (1 << 24)) return fail(RA_ERR_UNSUPPORTED, "at most 2^24 tokens per call");
-  if (!aligned(k, 16) || !aligned(v, 16)) return fail(RA_ERR_INVALID_ARG, "k or v NULL or not 16-byte aligned");
+  if (total > 0 && (!aligned(k, 16) || !aligned(v, 16))) return fail(RA_ERR_INVALID_ARG, "k or v NULL or not 16-byte aligned");
   if ((st = check_strides("k", k_token, k_head, total, p->Hkv)) != RA_OK) return st;
   if ((st = check_strides("v", v_token, v_head, total, p->Hkv)) != RA_OK) return st;
   if ((long long)total * p->Hkv >= (1ll << 33)) return fail(RA_ERR_UNSUPPORTED, "too many rows for one call");

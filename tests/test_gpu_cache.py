@@ -276,6 +276,60 @@ def test_refused_calls_change_nothing():
         c.attention(0, k.float(), ints([0]))
 
 
+@pytest.mark.parametrize("rows,tokens", [(3, 1), (3, 40), (3, 400), (300, 1), (300, 2)])
+def test_refused_writes_change_nothing(rows, tokens):
+    # short and long lists, few and many tokens: beside a bad entry nothing of the good ones is written
+    c, m = make(n_pages=rows * 27, page=16, max_seqs=rows + 2, max_pages=27)
+    every = list(range(rows))
+    c.extend(ints(every), ints([tokens + 5] * rows))
+    m.extend(every, [tokens + 5] * rows)
+    k, v = rand(5, rows * tokens, 2, D), rand(6, rows * tokens, 2, D)
+    cu = [i * tokens for i in range(rows + 1)]
+
+    def write(seqs, offsets=cu):
+        single = tokens == 1 and offsets is cu
+        c.write(0, ints(seqs), k, v, cu_new=None if single else ints(offsets))
+
+    def with_entry(values, i, x):
+        return values[:i] + [x] + values[i + 1:]
+
+    bounds = api.RA_ERR_DEVICE_BOUNDS
+    for i in (0, rows // 2, rows - 1):
+        for bad in (every[i - 1], rows + 2, -2, 2 ** 31 - 1, rows):         # twice, outside, a row without tokens
+            refused(c, m, bounds, lambda: write(with_entry(every, i, bad)))
+        for bad in (-1, -2 ** 31, 2 ** 31 - 1, rows * tokens + 1):
+            refused(c, m, bounds, lambda: write(every, with_entry(cu, i, bad)))
+    refused(c, m, bounds, lambda: write(every, with_entry(cu, 1, cu[2] + 1)))
+    refused(c, m, bounds, lambda: write(every, cu[:-1] + [rows * tokens + 1]))
+    refused(c, m, bounds, lambda: write(every, [0] * rows + [tokens + 6]))  # longer than the row
+    last = (tokens + 5 - 1) // 16
+    keep = int(c.table[rows - 1, last])
+    for bad in (-1, c.p.n_pages, 2 ** 31 - 1):
+        c.table[rows - 1, last] = bad
+        m.rows[rows - 1][last] = bad
+        before = c.pool.clone()
+        write(every)
+        with pytest.raises(api.RotateAttnError) as e:
+            c.check()
+        assert e.value.status == bounds and torch.equal(c.pool, before)
+    c.table[rows - 1, last] = m.rows[rows - 1][last] = keep
+    some = with_entry(every, 1, -1)                     # a padded list, whose tokens of the entry are passed over
+    write(some)
+    m.write(0, some, [tokens] * rows, k, v)
+    m.same()
+    write(every)
+    m.write(0, every, [tokens] * rows, k, v)
+    m.same()
+    inner = [1] + [min(2 + i * tokens, rows * tokens - 1) for i in range(rows)]   # tokens outside the offsets
+    c.write(0, ints(every), k, v, cu_new=ints(inner))
+    for r, (a, b) in enumerate(zip(inner, inner[1:])):
+        m.write(0, [r], [b - a], k[a:b], v[a:b])
+    m.same()
+    c.write(0, ints(every), k[:0], v[:0], cu_new=ints([0] * (rows + 1)))
+    m.same()
+    refused(c, m, bounds, lambda: c.write(0, ints(every), k[:0], v[:0], cu_new=ints([0] * rows + [1])))
+
+
 # ---------------------------------------------------------------- attention
 
 def filled(lens, shared, page, hkv, dtype, seed, layers=1, nan_tail=True):
