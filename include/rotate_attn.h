@@ -379,7 +379,9 @@ ra_status ra_cache_extend(const ra_cache_problem *p, const ra_cache *c, const in
  * (elements; multiples of 8).  cu_new: int32 [n + 1], ascending within 0 ..
  * total; tokens outside it are passed over.  Nothing is written, and
  * RA_ERR_DEVICE_BOUNDS reported, also where cu_new descends or leaves that
- * range, a row is shorter than its tokens, or the table names no page for one.
+ * range, a row is shorter than its tokens, the table names no page for one, or
+ * the page is shared with another row, whose tokens it holds too (write before
+ * a fork, or behind it).
  * One launch for short lists, two otherwise. */
 ra_status ra_cache_write(const ra_cache_problem *p, const ra_cache *c, int layer, const int *seqs, const int *cu_new,
                          int n, int total, const void *k, const void *v, long long k_token, long long k_head,

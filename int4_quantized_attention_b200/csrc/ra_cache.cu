@@ -418,7 +418,8 @@ __device__ int check_write(const CacheProb& c, const int* seqs, const int* cu_ne
     const int len = c.lens[row], slot = ((len - count) >> c.page_shift) + j;
     if (slot > (len - 1) >> c.page_shift) continue;
     const int page = c.table[(long long)row * c.max_pages + slot];
-    if ((uint32_t)page >= (uint32_t)c.n_pages) bad = BAD;
+    // a page that other rows share holds their tokens too
+    if ((uint32_t)page >= (uint32_t)c.n_pages || c.refs[page] != 1) bad = BAD;
   }
   if (cu_new != nullptr) {   // entries without tokens or with bad offsets have no page of their own above
     int row, count;

@@ -330,6 +330,42 @@ def test_refused_writes_change_nothing(rows, tokens):
     refused(c, m, bounds, lambda: c.write(0, ints(every), k[:0], v[:0], cu_new=ints([0] * rows + [1])))
 
 
+@pytest.mark.parametrize("kids,pages", [(1, 2), (2, 90), (300, 2)])
+def test_writes_do_not_reach_shared_pages(kids, pages):
+    # the last tokens of a row lie in full pages that its forks share: neither side may overwrite them
+    page = 16
+    c, m = make(n_pages=pages + 3 * kids + 10, page=page, max_seqs=kids + 3, max_pages=pages + 2)
+    n = pages * page
+    children = list(range(1, kids + 1))
+    c.extend(ints([0, kids + 1]), ints([n, 5]))
+    m.extend([0, kids + 1], [n, 5])
+    c.fork(ints([0] * kids), ints(children))
+    m.fork([0] * kids, children)
+    bounds = api.RA_ERR_DEVICE_BOUNDS
+    k, v = rand(5, 2 * n, 2, D), rand(6, 2 * n, 2, D)
+    for row in (0, 1, kids):
+        for count in (1, page, page + 1, n):
+            refused(c, m, bounds, lambda: c.write(0, ints([kids + 1, row]), k[:2 + count], v[:2 + count],
+                                                  cu_new=ints([0, 2, 2 + count])))
+        refused(c, m, bounds, lambda: c.write(0, ints([row]), k[:1], v[:1]))
+    # what was written behind the fork is each row's own; a token further back is not
+    every = [0] + children
+    c.extend(ints(every), ints([3] * len(every)))
+    m.extend(every, [3] * len(every))
+    cu = [3 * i for i in range(len(every) + 1)]
+    kk, vv = rand(7, cu[-1] + 1, 2, D), rand(8, cu[-1] + 1, 2, D)
+    c.write(0, ints(every), kk[:-1], vv[:-1], cu_new=ints(cu))
+    m.write(0, every, [3] * len(every), kk, vv)
+    m.same()
+    refused(c, m, bounds, lambda: c.write(0, ints(every), kk, vv, cu_new=ints(cu[:-1] + [cu[-1] + 1])))
+    # the last row that still names the pages may write them
+    c.free(ints(every[:-1]))
+    m.free(every[:-1])
+    c.write(0, ints([kids]), k[:n + 3], v[:n + 3], cu_new=ints([0, n + 3]))
+    m.write(0, [kids], [n + 3], k, v)
+    m.same()
+
+
 # ---------------------------------------------------------------- attention
 
 def filled(lens, shared, page, hkv, dtype, seed, layers=1, nan_tail=True):
