@@ -106,13 +106,13 @@ __device__ Scan cluster_scan(int need, int pages, int flags, Shared* sh) {
 
 struct Ws {
   WsHeader* hdr;
-  int *jobs, *mark, *rank, *list, *map, *src, *dst, *rows;
+  int *jobs, *mark, *held, *rank, *list, *map, *src, *dst, *rows;
 };
 __host__ Ws ws_of(const CacheProb& c, void* ws) {
   const CacheWs L = cache_ws(c.n_pages, c.max_seqs);
   char* b = static_cast<char*>(ws);
   auto at = [&](size_t o) { return reinterpret_cast<int*>(b + o); };
-  return {static_cast<WsHeader*>(ws), at(L.jobs), at(L.mark), at(L.rank), at(L.list), at(L.map), at(L.src),
+  return {static_cast<WsHeader*>(ws), at(L.jobs), at(L.mark), at(L.held), at(L.rank), at(L.list), at(L.map), at(L.src),
           at(L.dst), at(L.rows)};
 }
 
@@ -179,9 +179,29 @@ __device__ __forceinline__ bool refused(const Scan& s, WsHeader* h, uint32_t sit
   return true;
 }
 
+// A write that follows a refused extend in the stream would find no slots of its
+// own and store over the row's last tokens.  So a refused extend leaves the rows
+// it named in w.held, and writes pass those over, until a call gives the row
+// slots or empties it, or the error has been read.  w.held means something only
+// while the error word has DEVERR_HELD, since its contents are unspecified before.
+// Only extend sets that bit, behind all of its threads' reading it.
+__device__ __forceinline__ bool holding(const Ws& w) { return (w.hdr->err.word & DEVERR_HELD) != 0; }
+// All threads of the cluster, after a refusal; `already` as the call found it.
+__device__ void hold_rows(const CacheProb& c, const Ws& w, const int* rows, int n, bool already) {
+  const int at = ctarank() * CT + threadIdx.x;
+  if (!already) {
+    for (int r = at; r < c.max_seqs; r += ALL) w.held[r] = 0;
+    cluster_barrier();
+  }
+  for (int i = at; i < n; i += ALL)
+    if (rows[i] >= 0 && rows[i] < c.max_seqs) w.held[rows[i]] = 1;
+  if (at == 0) atomicOr(&w.hdr->err.word, DEVERR_HELD);
+}
+
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
     extend_kernel(CacheProb c, const int* __restrict__ seqs, const int* __restrict__ n_new, int n, Ws w) {
   __shared__ Shared sh;
+  const bool held = holding(w);
   int flags = check_rows(c, w, seqs, n, nullptr);
   // entries in list order, a run of consecutive ones per thread
   const int per = (n + ALL - 1) / ALL, at = ctarank() * CT + threadIdx.x;
@@ -196,7 +216,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
   }
   const Run run = page_run(c);
   const Scan s = cluster_scan(need, count_free(c, run), flags, &sh);
-  if (refused(s, w.hdr, 0x5001)) return;
+  if (refused(s, w.hdr, 0x5001)) return hold_rows(c, w, seqs, n, held);
   list_free(c, w, run, s.before.pages, s.all.need);
   int r = s.before.need;
   for (int i = i0; i < i1; ++i) {
@@ -215,13 +235,17 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
       c.refs[page] = 1;
     }
     __syncwarp();
-    if (lane == 0) c.lens[row] = len + n_new[i];
+    if (lane == 0) {
+      c.lens[row] = len + n_new[i];
+      if (held) w.held[row] = 0;
+    }
   }
 }
 
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
     fork_kernel(CacheProb c, const int* __restrict__ parents, const int* __restrict__ children, int n, Ws w) {
   __shared__ Shared sh;
+  const bool held = holding(w);
   int flags = check_rows(c, w, children, n, parents);
   const int per = (n + ALL - 1) / ALL, at = ctarank() * CT + threadIdx.x;
   if (at == 0) w.jobs[0] = 0;   // nothing to copy if this call is refused
@@ -270,6 +294,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
         }
       }
       c.lens[child] = len;
+      if (held) w.held[child] = 0;
     }
   }
   if (at == 0) w.jobs[0] = s.all.need;
@@ -278,6 +303,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
     free_kernel(CacheProb c, const int* __restrict__ seqs, int n, Ws w) {
   __shared__ Shared sh;
+  const bool held = holding(w);
   if (refused(cluster_scan(0, 0, check_rows(c, w, seqs, n, nullptr), &sh), w.hdr, 0x5021)) return;
   const int lane = threadIdx.x & 31, at = ctarank() * CT + threadIdx.x;
   for (int i = at >> 5; i < n; i += ALL / 32) {
@@ -292,7 +318,10 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
       t[k] = -1;
     }
     __syncwarp();
-    if (lane == 0) c.lens[row] = 0;
+    if (lane == 0) {
+      c.lens[row] = 0;
+      if (held) w.held[row] = 0;
+    }
   }
 }
 
@@ -377,7 +406,9 @@ __global__ void __launch_bounds__(256) copy_kernel(CacheProb c, Ws w, int remap)
 // one thread for each entry of the list and for each page that the tokens lie
 // in; `at` of `all` threads call this.  Rows named twice are found elsewhere.
 // Returns BAD or 0, by thread.
-__device__ int check_write(const CacheProb& c, const int* seqs, const int* cu_new, int n, int total, int at, int all) {
+__device__ int check_write(const CacheProb& c, const Ws& w, const int* seqs, const int* cu_new, int n, int total, int at,
+                           int all) {
+  const bool held = holding(w);
   int bad = 0;
   auto entry = [&](int i, int& row, int& count) {   // false: nothing of it is written
     row = seqs[i];
@@ -391,6 +422,7 @@ __device__ int check_write(const CacheProb& c, const int* seqs, const int* cu_ne
       count = b - a;
     }
     if (row == -1) return false;
+    if (held && row >= 0 && row < c.max_seqs && w.held[row] != 0) return false;
     if (!row_ok(c, row) || c.lens[row] < count) {
       bad = BAD;
       return false;
@@ -434,7 +466,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
   __shared__ Shared sh;
   dependents_may_start();
   const int at = ctarank() * CT + threadIdx.x;
-  const int flags = check_rows(c, w, seqs, n, nullptr) | check_write(c, seqs, cu_new, n, total, at, ALL);
+  const int flags = check_rows(c, w, seqs, n, nullptr) | check_write(c, w, seqs, cu_new, n, total, at, ALL);
   const bool no = refused(cluster_scan(0, 0, flags, &sh), w.hdr, 0x5041);
   if (at == 0) w.jobs[1] = !no;
 }
@@ -456,7 +488,7 @@ __global__ void __launch_bounds__(CHECKED ? WRITE_CT : 2 * WRITE_CT)
   if (!CHECKED && threadIdx.x >= WRITE_CT) {
     const int me = threadIdx.x - WRITE_CT, row = me < n ? seqs[me] : -1;
     rows[me] = row;
-    bad = check_write(c, seqs, cu_new, n, total, me, WRITE_CT);
+    bad = check_write(c, w, seqs, cu_new, n, total, me, WRITE_CT);
     asm volatile("bar.sync 1, %0;" ::"n"(WRITE_CT) : "memory");
     if (row != -1) {
 #pragma unroll 8
@@ -468,6 +500,7 @@ __global__ void __launch_bounds__(CHECKED ? WRITE_CT : 2 * WRITE_CT)
     const int lane16 = threadIdx.x & 15;
     const long long unit = ((long long)blockIdx.x * WRITE_CT + threadIdx.x) >> 4;
     const int per = 2 * c.Hkv;
+    const bool held = holding(w);
     if (unit < (long long)total * per) {
       const int t = (int)(unit / per), part = (int)(unit % per), head = part % c.Hkv;
       const bool is_v = part >= c.Hkv;
@@ -486,7 +519,7 @@ __global__ void __launch_bounds__(CHECKED ? WRITE_CT : 2 * WRITE_CT)
       if (first >= 0 && t >= first && t < last && row != -1 && row_ok(c, row) && c.lens[row] >= last - first) {
         const int pos = c.lens[row] - (last - t);
         const int page = c.table[(long long)row * c.max_pages + (pos >> c.page_shift)];
-        if ((uint32_t)page < (uint32_t)c.n_pages) {
+        if ((uint32_t)page < (uint32_t)c.n_pages && !(held && w.held[row] != 0)) {
           const long long slot = (((long long)layer * c.n_pages + page) * c.Hkv + head) * c.page_size + (pos & (c.page_size - 1));
           x = reinterpret_cast<const uint4*>(is_v ? v + t * v_tok + head * v_head : k + t * k_tok + head * k_head)[lane16];
           dst = reinterpret_cast<uint4*>((is_v ? c.v : c.k) + slot * 256) + lane16;

@@ -13,7 +13,7 @@ struct CacheProb {
 
 // Workspace of the page operations (after the 256-byte header).
 struct CacheWs {
-  size_t jobs, mark, rank, list, map, src, dst, rows, total;
+  size_t jobs, mark, held, rank, list, map, src, dst, rows, total;
 };
 inline CacheWs cache_ws(int n_pages, int max_seqs) {
   CacheWs L;
@@ -23,6 +23,8 @@ inline CacheWs cache_ws(int n_pages, int max_seqs) {
   L.jobs = o;
   o += 256;
   L.mark = o;
+  o += seqs;
+  L.held = o;
   o += seqs;
   L.rank = o;
   o += seqs;

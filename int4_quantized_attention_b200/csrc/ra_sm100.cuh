@@ -14,6 +14,7 @@ enum : uint32_t {
   DEVERR_BOUNDS = 1u << 1,      // a self-check found an index out of range
   DEVERR_WORKSPACE = 1u << 2,   // workspace signature does not match the problem
   DEVERR_FULL = 1u << 3,        // a cache has too few free pages, or a sequence too few table entries
+  DEVERR_HELD = 1u << 4,        // beside one of the others: a cache's workspace lists rows that take no writes
 };
 
 struct DeviceErr {

@@ -366,6 +366,102 @@ def test_writes_do_not_reach_shared_pages(kids, pages):
     m.same()
 
 
+def full(c, status=api.RA_ERR_CACHE_FULL):
+    with pytest.raises(api.RotateAttnError) as e:
+        c.check()
+    assert e.value.status == status
+
+
+@pytest.mark.parametrize("many", [1, 300])
+def test_writes_behind_a_refused_extend(many):
+    # the tokens had no slots: nothing of the row's own is overwritten, whatever else the stream does
+    page, rows = 16, many + 5
+    c, m = make(layers=2, n_pages=3 * rows - 1, page=page, max_seqs=rows, max_pages=3 * rows)
+    c._work[256:] = 0x77
+    every = list(range(rows - 1))                           # the last row stays empty
+    c.extend(ints(every), ints([40] * len(every)))
+    m.extend(every, [40] * len(every))                      # 3 pages of a row, 2 are left
+    for layer in range(2):
+        k, v = rand(layer, 40 * len(every), 2, D), rand(9 + layer, 40 * len(every), 2, D)
+        c.write(layer, ints(every), k, v, cu_new=ints([40 * i for i in range(rows)]))
+        m.write(layer, every, [40] * len(every), k, v)
+    m.same()
+    a, b = every[:many], every[many:]                       # two lists of a step; the first wants too much
+    k, v = rand(20, many * 9, 2, D), rand(21, many * 9, 2, D)
+    write = lambda seqs, n=1: c.write(1, ints(seqs), k[:n * len(seqs)], v[:n * len(seqs)], cu_new=None if n == 1 else   # noqa: E731
+                                      ints([n * i for i in range(len(seqs) + 1)]))
+    c.extend(ints(a), ints([50] * many))                         # 3 more each
+    c.extend(ints(b), ints([1] * len(b)))
+    m.extend(b, [1] * len(b))
+    write(a)
+    write(a, 9)
+    k2, v2 = rand(22, len(b) + many, 2, D), rand(23, len(b) + many, 2, D)
+    c.write(1, ints(a + b), k2, v2)                         # one list with both
+    m.write(1, [-1] * many + b, [1] * len(every), k2, v2)
+    full(c)
+    m.same()
+    # once read, the error holds nothing back: the last token may be written again
+    write(a)
+    m.write(1, a, [1] * many, k, v)
+    m.same()
+    # a second refusal holds its own rows alone
+    c.extend(ints([b[0]]), ints([2 ** 20]))
+    write(a)
+    write([b[0]])
+    m.write(1, a, [1] * many, k, v)
+    full(c)
+    m.same()
+    # so does one for another reason
+    c.extend(ints([b[0], b[0]]), ints([1, 1]))
+    write([b[0]])
+    full(c, api.RA_ERR_DEVICE_BOUNDS)
+    m.same()
+    # an extend that is carried out gives the row its slots; the error stands until it is read
+    c.extend(ints([b[0], b[1], rows - 1]), ints([2 ** 20, 0, 0]))
+    c.extend(ints([b[0]]), ints([2]))
+    write([b[0]], 2)
+    write([b[1]])
+    m.extend([b[0]], [2])
+    m.write(1, [b[0]], [2], k, v)
+    # so do a free and a fork
+    c.free(ints([b[1]]))
+    m.free([b[1]])
+    c.fork(ints([b[0]]), ints([rows - 1]))
+    m.fork([b[0]], [rows - 1])
+    write([rows - 1])
+    m.write(1, [rows - 1], [1], k, v)
+    full(c)
+    m.same()
+
+
+def test_captured_step_on_a_full_cache():
+    # extend and write in one graph: replays beyond the last page leave the cache as it was
+    c, m = make(n_pages=4, page=16, max_seqs=2, max_pages=4)
+    c.extend(ints([0, 1]), ints([30, 30]))
+    m.extend([0, 1], [30, 30])
+    s, one, k, v = ints([0, 1]), ints([1, 1]), rand(1, 2, 2, D), rand(2, 2, 2, D)
+
+    def step():
+        c.extend(s, one)
+        c.write(0, s, k, v)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for r in range(2):
+        k.copy_(rand(30 + r, 2, 2, D))
+        graph.replay()
+        m.extend([0, 1], [1, 1])
+        m.write(0, [0, 1], [1, 1], k, v)
+        m.same()
+    for r in range(3):
+        k.copy_(rand(40 + r, 2, 2, D))
+        graph.replay()
+        if r != 1:                                          # read, or not, before the next replay
+            full(c)
+            m.same()
+
+
 # ---------------------------------------------------------------- attention
 
 def filled(lens, shared, page, hkv, dtype, seed, layers=1, nan_tail=True):
