@@ -509,16 +509,21 @@ ra_status ra_cache_attention_fwd(const ra_cache_problem* p, const ra_cache* c, c
   // one head per warp while that fits the SMs at once; more per lookup else
   P.join_heads = (long long)a->total_q * a->Hq <= 64ll * SM_BOUND ? 8 : 32;
   P.lead_only = cu_q == nullptr && P.G <= ra::FEW_ROWS;
-  // A short shared region leaves SMs to the kernel of few rows, which runs
-  // beside it: LEAD_TILES of its key tiles per SM (a call of 61 sequences
-  // behind 2048 tokens: 51 us one after the other).
+  // A short shared region, of at most LEAD_TILES key tiles per SM on half of
+  // them, leaves the others to the kernel of few rows, which runs beside it (the
+  // host does not know the own lengths, but with half of the SMs they take at most
+  // twice their time); a longer one gets the whole GPU, and so does the kernel of
+  // few rows behind it.  Beside / one after the other: own lengths 1 to 1024 of 61
+  // rows, 32/8 heads, 2048 shared tokens (43 SMs) 31 / 44 us, 2944 (62 SMs) 35 /
+  // 45; 5683 to 15646 of 25 rows, 40/8 heads, 237 / 202 and 285 / 210.  (Beside a
+  // region on all SMs but one they take 22 ms.)
   constexpr long long LEAD_TILES = 3;
   P.many.grid = many ? sms : 0;
   if (many && P.lead_only) {
     const long long tiles = (long long)((a->shared + ra::KEYS - 1) / ra::KEYS) * p->Hkv *
                             ((a->total_q + 2 * P.TQ - 1) / (2 * P.TQ));
     const long long want = (tiles + LEAD_TILES - 1) / LEAD_TILES;
-    if (want < sms) P.many.grid = (int)want;
+    if (want <= sms / 2) P.many.grid = (int)want;
   }
   P.few.grid = few ? ra::FEW_CTAS * (P.many.grid < sms ? sms - P.many.grid : sms) : 0;
   ra::SeqMaps m;

@@ -659,6 +659,39 @@ def test_wide_batch_long_prefix(hq, hkv):
     run_attention(c, m, list(range(150)), [1] * 150, hq, 4096)
 
 
+def test_time_rises_with_the_shared_part_and_does_not_jump():
+    # long own parts behind shared parts of any length: never the few SMs that a shared part would leave, but
+    # half of them or all, so at most twice the time that they take after a longer shared part
+    rows, own, page, longest = 25, 8000, 64, 8192
+    pages = -(-own // page)
+    c = api.PagedCache(1, longest // page + rows * pages, page, 8, rows, longest // page + pages, dtype=BF16)
+    c.pool.normal_()
+    q, s = rand(1, rows, 40, D, dtype=BF16), ints(list(range(rows)))
+    at = torch.arange(rows * pages, device="cuda", dtype=torch.int32).view(rows, pages) + longest // page
+
+    def took(shared):
+        lead = shared // page
+        c.table.fill_(-1)
+        c.table[:, :lead] = torch.arange(lead, device="cuda", dtype=torch.int32)
+        c.table[:, lead:lead + pages] = at
+        c.lens.fill_(shared + own)
+        times = []
+        for _ in range(6):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(5):
+                c.attention(0, q, s, shared=shared)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times[1:])
+
+    whole = took(longest)                               # about 0.2 ms a call
+    for shared in (128, 1024, 1984, 2304, 3008, 3392, 3520, 4096, 5120, 6144, 6912, 7040, 7104):
+        assert took(shared) < 2 * whole, shared
+    c.check()
+
+
 @pytest.mark.parametrize("shared", [0, 2048])
 def test_nan_queries_and_hidden_values(shared):
     # drafted tokens: a value that only the later ones see; a NaN query beside others
