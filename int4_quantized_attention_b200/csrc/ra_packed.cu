@@ -462,13 +462,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         free_segment(k);
         continue;
       }
-      // this row's limit, and the smallest of the tile's (the same in its four warps)
+      // this row's limit, and the smallest of the tile's (the same in its four
+      // warps; of both tiles' in the shared region, where limits do not ascend)
       const int t0 = g.tok + X * P.TQ, t1 = min(t0 + P.TQ, g.tok + g.ntok);
       int lim, gmin;
       if (g.lead) {
         lim = row_limit(P, 1, 0, g.len, min(tt, t1 - 1));
         gmin = g.len;
-        for (int t = t0 + lane; t < t1; t += 32) gmin = min(gmin, row_limit(P, g.lead, g.off, g.len, t));
+        for (int t = g.tok + lane; t < g.tok + g.ntok; t += 32) gmin = min(gmin, row_limit(P, g.lead, g.off, g.len, t));
         gmin = __reduce_min_sync(0xffffffffu, gmin);
       } else {
         lim = row_limit(P, 0, g.off, g.len, min(tt, t1 - 1));
@@ -482,8 +483,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // S(t) has landed -- and with it P.V(t-1)
         if (!(ok = wait_all(B_SFULL + X, s_phase & 1, 0x4102))) break;
         ++s_phase;
-        if (gmin < key + KEYS) {
-          // a tile that some row sees in part: this warp's 32 V rows
+        if (gmin < key + KEYS && (X == 0 || t >= g.n[0])) {
+          // a tile that some row sees in part: this warp's 32 V rows.  Tile A's
+          // warps do it where A has the tile: B's gmin is not below A's, and B's
+          // product comes after A's, which waits for these warps' P.  So no
+          // product reads V while it changes.
           const int ring = g.ring + t;
           if (!(ok = wait_all(B_VFULL + ring % STAGES, (ring / STAGES) & 1, 0x4103))) break;
           uint8_t* vt = sm + Smem::V + (ring % STAGES) * 32768;

@@ -714,6 +714,31 @@ def test_nan_queries_and_hidden_values(shared):
     check(lse, wl, tl, "lse")
 
 
+@pytest.mark.parametrize("first_short", [True, False])
+def test_infinities_in_the_shared_part_beside_shorter_rows(first_short):
+    # rows that end inside the shared pages beside rows that see a value of infinity there with a weight that
+    # vanishes: the same result every time, whichever query tile comes first
+    n, shared, page = 64, 512, 16                       # 4 heads per key head: 32 tokens are a query tile
+    c, m = filled([5] * n, shared, page, 1, BF16, seed=27, nan_tail=False)
+    short = [i for i in range(n) if (i < 32) == first_short]
+    for i in short:
+        c.lens[i] = 100
+        m.lens[i], m.rows[i] = 100, m.rows[i][:7]
+    q = rand(4, n, 4, D, dtype=BF16).abs()
+    for tile in range(1, 4):                            # in each tile that only the longer rows see
+        where = c.table[short[0] ^ 32, (128 * tile + 40) // page].long(), (128 * tile + 40) % page
+        c.pool[0, 0, where[0], 0, where[1]] = -30.0     # scores below -1000
+        c.pool[1, 0, where[0], 0, where[1], 10 * tile] = math.inf
+    cu = list(range(n + 1))
+    want, wl, tol, tl = paged(c.pool, 0, m.rows, m.lens, q, list(range(n)), cu)
+    assert int((want == math.inf).sum()) == 3 * 32 * 4
+    for _ in range(20):
+        o, lse = c.attention(0, q, ints(list(range(n))), shared=shared, return_lse=True)
+        c.check()
+        check(o, want, tol, "o")
+        check(lse, wl, tl, "lse")
+
+
 def test_layers_scale_and_peaked_scores():
     c, m = filled([500, 3], 128, 64, 2, F16, seed=14, layers=3)
     run_attention(c, m, [0, 1], [1, 1], 4, 128, layer=2, scale=0.5, gain=10.0)
