@@ -317,8 +317,11 @@ size_t ra_packed_workspace_bytes(const ra_packed *p);
  * 1], ascending from 0; lse: device float [total_q][Hq], the natural
  * logarithm of each row's sum, or NULL.  The lengths are read on the device
  * alone: a captured call replays with the lengths of its moment.  Offsets
- * that descend or leave the buffers are reported (RA_ERR_DEVICE_BOUNDS) and
- * that sequence is left out. */
+ * that descend or leave the buffers are always reported
+ * (RA_ERR_DEVICE_BOUNDS).  That sequence is left out; the rows of the others
+ * may then be left out too, or hold the result of another sequence that lays
+ * claim to them, since they are found by the order of the offsets.  No memory
+ * but the rows of o and lse is written. */
 ra_status ra_packed_attention_fwd(const ra_packed *p, const void *q, const void *k, const void *v, const int *cu_q,
                                   const int *cu_k, void *o, float *lse, void *workspace, size_t workspace_bytes,
                                   ra_stream stream);

@@ -683,6 +683,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       q0 += g.n[0] > 0;
       q1 += g.n[1] > 0;
     }
+    if (!P.split && P.n_seqs > LPT_SEQS) {   // sequences that the list passed by are looked at too, for what they report
+      for (int i = blockIdx.x * 32 + lane; i < P.n_seqs; i += gridDim.x * 32) seq_info(P, i, err);
+    }
     if (!P.split && lane == 0) {   // no CTA takes a ticket after its last: the last one out sets them back
       __threadfence();
       if (atomicAdd(&hdr->leaving, 1u) == gridDim.x - 1) {

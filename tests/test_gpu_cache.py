@@ -772,6 +772,23 @@ def test_bad_pages_are_reported():
     c.check()
 
 
+@pytest.mark.parametrize("shared", [0, 128])
+@pytest.mark.parametrize("hq", [2, 64])
+def test_a_bad_query_offset_is_reported(shared, hq):
+    n = 150
+    c, m = filled([50 + i % 9 for i in range(n)], shared, 16, 2, F16, seed=28)
+    seqs, counts = list(range(n)), [1 + i % 3 for i in range(n)]
+    cu = [0] + list(itertools.accumulate(counts))
+    q = rand(3, cu[-1], hq, D)
+    for at in (1, n // 2, n - 1, n):
+        for bad in (-1, -2 ** 31, cu[at - 1] - 1, cu[-1] + 1, 2 ** 31 - 1):
+            c.attention(0, q, ints(seqs), cu_q=ints(cu[:at] + [bad] + cu[at + 1:]), shared=shared)
+            with pytest.raises(api.RotateAttnError) as e:
+                c.check()
+            assert e.value.status == api.RA_ERR_DEVICE_BOUNDS
+    run_attention(c, m, seqs, counts, hq, shared)
+
+
 @pytest.mark.parametrize("shared", [0, 32])
 def test_lengths_near_the_largest_int_are_reported(shared):
     # a length that no table row holds leaves the sequence out, also where one page more passes 2^31

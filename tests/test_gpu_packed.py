@@ -262,6 +262,30 @@ def test_bad_offsets_are_reported_and_left_out(op):
     op.check()
 
 
+@pytest.mark.parametrize("n,hq", [(300, 48), (300, 2), (129, 48), (60, 48), (40, 2)])
+def test_a_bad_offset_anywhere_is_reported(op, n, hq):
+    # among many sequences, whole items or split ones; a plain call afterwards is right
+    lens = [40 + i % 7 for i in range(n)]
+    cu = cum(lens)
+    q, k, v = inputs(2, cu[-1], cu[-1], hq, 2, F16)
+    for at in sorted({1, n // 4, n // 2, n // 2 + 1, n - 1, n}):
+        for bad in (0, -1, -2 ** 31, cu[at - 1] - 1, cu[-1] + 1, 2 ** 31 - 1):
+            if (at, bad) == (1, 0):                     # an empty first sequence
+                continue
+            for which in "qk":
+                wrong = cu[:at] + [bad] + cu[at + 1:]
+                out = torch.full_like(q, 2.0)
+                op.forward(q, k, v, ints(wrong if which == "q" else cu), ints(wrong if which == "k" else cu), out=out)
+                with pytest.raises(api.RotateAttnError) as e:
+                    op.check()
+                assert e.value.status == api.RA_ERR_DEVICE_BOUNDS, (at, bad, which)
+    o, lse = op.forward(q, k, v, ints(cu), ints(cu), return_lse=True)
+    op.check()
+    want, wl, tol, tl = packed(q, k, v, cu, cu, True)
+    check(o, want, tol, "o")
+    check(lse, wl, tl, "lse")
+
+
 def test_no_tokens(op):
     q, k, v = inputs(2, 0, 4, 2, 2, F16)
     assert op.forward(q, k, v, ints([0, 0]), ints([0, 4])).shape == (0, 2, D)
