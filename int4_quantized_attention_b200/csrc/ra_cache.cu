@@ -165,7 +165,7 @@ __device__ __forceinline__ int count_free(const CacheProb& c, Run r) {
 // The first `want` free pages, lowest first, into w.list.
 __device__ __forceinline__ void list_free(const CacheProb& c, const Ws& w, Run r, int rank, int want) {
   for (int p = r.p0; p < r.p1 && rank < want; ++p)
-    if (c.refs[p] == 0) w.list[rank++] = p;
+    if (c.refs[p] == 0 && in_bounds(rank >= 0 && rank < c.n_pages, &w.hdr->err, 0x5101)) w.list[rank++] = p;
 }
 
 __device__ __forceinline__ void report_once(WsHeader* h, uint32_t bit, uint32_t site) {
@@ -230,7 +230,9 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
     if (row == -1) continue;
     const int len = c.lens[row], have = pages_for(c, len), more = pages_for(c, len + n_new[i]) - have, first = w.rank[i];
     for (int k = lane; k < more; k += 32) {
+      if (!in_bounds(first + k < c.n_pages && have + k < c.max_pages, &w.hdr->err, 0x5102)) continue;
       const int page = w.list[first + k];
+      if (!in_bounds(page >= 0 && page < c.n_pages, &w.hdr->err, 0x5103)) continue;
       c.table[(long long)row * c.max_pages + have + k] = page;
       c.refs[page] = 1;
     }
@@ -274,13 +276,14 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT)
     const int* from = c.table + (long long)parent * c.max_pages;
     int* to = c.table + (long long)child * c.max_pages;
     for (int k = lane; k < full; k += 32) {
+      if (!in_bounds(k < c.max_pages, &w.hdr->err, 0x5104)) continue;
       const int page = from[k];
       to[k] = page;
       if ((uint32_t)page < (uint32_t)c.n_pages) atomicAdd(&c.refs[page], 1);
       else report(&w.hdr->err, DEVERR_BOUNDS, 0x5014);
     }
     if (lane == 0) {
-      if (rest != 0) {
+      if (rest != 0 && in_bounds(full < c.max_pages && w.rank[i] >= 0 && w.rank[i] < c.n_pages, &w.hdr->err, 0x5105)) {
         const int page = w.list[w.rank[i]], old = from[full];
         to[full] = page;
         c.refs[page] = 1;
@@ -343,12 +346,13 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT) compact_kernel(
   for (int p = run.p0; p < run.p1; ++p) {
     const bool is = c.refs[p] != 0;
     w.map[p] = p;
-    if (!is && p < total) w.dst[h++] = p;
-    if (is && p >= total) w.src[m++] = p;
+    if (!is && p < total && in_bounds(h >= 0 && h < c.n_pages, &w.hdr->err, 0x5106)) w.dst[h++] = p;
+    if (is && p >= total && in_bounds(m >= 0 && m < c.n_pages, &w.hdr->err, 0x5107)) w.src[m++] = p;
   }
   cluster_barrier();
   for (int i = at; i < n; i += ALL) {
     const int from = w.src[i], to = w.dst[i];
+    if (!in_bounds((uint32_t)from < (uint32_t)c.n_pages && (uint32_t)to < (uint32_t)c.n_pages, &w.hdr->err, 0x5108)) continue;
     w.map[from] = to;
     w.rows[i] = c.page_size;
     c.refs[to] = c.refs[from];
@@ -384,6 +388,9 @@ __global__ void __launch_bounds__(256) copy_kernel(CacheProb c, Ws w, int remap)
   for (long long run = warp; run < runs; run += warps) {
     const int job = (int)(run / per), part = (int)(run % per);
     const int head = part % c.Hkv, layer = (part / c.Hkv) % c.layers;
+    if (!in_bounds((uint32_t)w.src[job] < (uint32_t)c.n_pages && (uint32_t)w.dst[job] < (uint32_t)c.n_pages &&
+                       w.rows[job] >= 0 && w.rows[job] <= c.page_size && layer < c.layers, &w.hdr->err, 0x5109))
+      continue;
     uint8_t* pool = part / c.Hkv >= c.layers ? c.v : c.k;
     const long long base = (long long)layer * c.n_pages * page_bytes + head * head_bytes;
     const uint4* src = reinterpret_cast<const uint4*>(pool + base + w.src[job] * page_bytes) + lane;
@@ -521,8 +528,11 @@ __global__ void __launch_bounds__(CHECKED ? WRITE_CT : 2 * WRITE_CT)
         const int page = c.table[(long long)row * c.max_pages + (pos >> c.page_shift)];
         if ((uint32_t)page < (uint32_t)c.n_pages && !(held && w.held[row] != 0)) {
           const long long slot = (((long long)layer * c.n_pages + page) * c.Hkv + head) * c.page_size + (pos & (c.page_size - 1));
-          x = reinterpret_cast<const uint4*>(is_v ? v + t * v_tok + head * v_head : k + t * k_tok + head * k_head)[lane16];
-          dst = reinterpret_cast<uint4*>((is_v ? c.v : c.k) + slot * 256) + lane16;
+          if (in_bounds(slot < (long long)c.layers * c.n_pages * c.Hkv * c.page_size && pos >> c.page_shift < c.max_pages,
+                        &w.hdr->err, 0x510a)) {
+            x = reinterpret_cast<const uint4*>(is_v ? v + t * v_tok + head * v_head : k + t * k_tok + head * k_head)[lane16];
+            dst = reinterpret_cast<uint4*>((is_v ? c.v : c.k) + slot * 256) + lane16;
+          }
         }
       }
     }

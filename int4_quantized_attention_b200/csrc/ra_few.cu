@@ -115,7 +115,9 @@ __global__ void __launch_bounds__(THREADS, FEW_CTAS) few_kernel(const __grid_con
             page = -1;
           }
         }
-        there = there && page >= 0;
+        there = there && page >= 0 &&
+                in_bounds(slot < P.max_pages && table_row < P.max_seqs && part.kvh < P.Hkv &&
+                              head_off + (pos & (P.page_size - 1)) * 256 + 256 <= P.v_page, err, 0x4504);
         const long long at = there ? page * P.v_page + head_off + (pos & (P.page_size - 1)) * 256 + copy_piece * 16 : 0;
         copy16(k_dst + tile_off(r, copy_piece), P.k + at, there);
         copy16(v_dst + tile_off(r, copy_piece), P.v + at, there);
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, FEW_CTAS) few_kernel(const __grid_con
       const int t = over_G(P, tid), token = q0 + t, head = part.kvh * P.G + tid - t * P.G;
       const RowOut out = row_out(P, P.few, part.out, part.slot, token, head, tid, FEW_ROWS);
       const float lse2 = L != 0.0f ? M - BIAS + log2f(L) : -INFINITY;
-      if (out.lse != nullptr && in_bounds(token < P.total_q && head < P.Hq, err, 0x4503))
+      if (out.lse != nullptr && in_bounds(row_inside(P, P.few, part.out, part.slot, token, head, tid, FEW_ROWS), err, 0x4503))
         *out.lse = part.out == OUT_FINAL ? lse2 * LN2 : lse2;
     }
     __syncthreads();
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(THREADS, FEW_CTAS) few_kernel(const __grid_con
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = z[e];
       }
-      if (in_bounds(token < P.total_q && head < P.Hq, err, 0x4502))
+      if (in_bounds(row_inside(P, P.few, part.out, part.slot, token, head, row, FEW_ROWS), err, 0x4502))
         store8<BF16>(row_out(P, P.few, part.out, part.slot, token, head, row, FEW_ROWS), c8, y);
     }
     __syncthreads();   // the ring is free for the next part

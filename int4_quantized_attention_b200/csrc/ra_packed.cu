@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const float inv = l != 0.0f ? 1.0f / l : 0.0f;
       const float lse2 = l != 0.0f ? m - BIAS + log2f(l) : -INFINITY;
       const int token = g.q0 + tt, head = g.kvh * P.G + rhead;
-      const bool store = valid && in_bounds(token >= 0 && token < P.total_q && head < P.Hq, err, 0x4105);
+      const bool store = valid && in_bounds(row_inside(P, P.many, g.out, g.slot, token, head, X * 128 + r, SLOT_ROWS), err, 0x4105);
       const int nf = *reinterpret_cast<volatile int*>(&mi->nf_tile[k % SEGS]);
       const RowOut out = row_out(P, P.many, g.out, g.slot, store ? token : 0, store ? head : 0, X * 128 + r);
       if (store && out.lse != nullptr) *out.lse = g.out == OUT_FINAL ? lse2 * LN2 : lse2;
@@ -732,6 +732,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       auto page_of = [&](int t) {
         const int first = (g.tile0 + t) * KEYS + (box_page << P.page_shift);
         if (t >= nload || box_page >= KEYS >> P.page_shift || first >= len) return -1;
+        if (!in_bounds(g.row >= 0 && g.row < P.max_seqs && (key0 + first) >> P.page_shift < P.max_pages, err, 0x4210))
+          return P.n_pages;
         const int page = trow[(key0 + first) >> P.page_shift];
         if ((uint32_t)page < (uint32_t)P.n_pages) return page;
         report(err, DEVERR_BOUNDS, 0x4204);   // not a page: read as zeros
@@ -890,10 +892,11 @@ struct Parts {           // part c lies at first + c step (+ back for c = 0)
   const float *o, *l;
   long long first, step, back;
   int n;
+  long long rows;      // of the buffer
 };
 __device__ __forceinline__ Parts slot_parts(const ShareBuf& b, int slot_rows, int cta, int n, int row) {
   // the item goes on behind the first CTA's share (slot 1), began before the others' (slot 0)
-  return {b.slot_o, b.slot_lse, 2ll * cta * slot_rows + row, 2ll * slot_rows, slot_rows, n};
+  return {b.slot_o, b.slot_lse, 2ll * cta * slot_rows + row, 2ll * slot_rows, slot_rows, n, 2ll * b.grid * slot_rows};
 }
 template <bool BF16>
 __device__ __forceinline__ void join_row(const SeqProb& P, const Parts& a, const Parts& b, int token, int head, int lane) {
@@ -913,6 +916,7 @@ __device__ __forceinline__ void join_row(const SeqProb& P, const Parts& a, const
       const Parts& p = c < a.n ? a : b;
       const int d = c < a.n ? c : c - a.n;
       const long long at = p.first + d * p.step + (d == 0 ? p.back : 0);
+      if (!in_bounds(at >= 0 && at < p.rows, P.err, 0x4601)) continue;
       l[k] = p.l[at];
       x[k] = reinterpret_cast<const float4*>(p.o + at * D)[lane];
     }
@@ -932,6 +936,7 @@ __device__ __forceinline__ void join_row(const SeqProb& P, const Parts& a, const
       acc.w = fmaf(w, x[k].w, acc.w);
     }
   }
+  if (!in_bounds(token >= 0 && token < P.total_q && head >= 0 && head < P.Hq, P.err, 0x4602)) return;
   const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
   const uint2 out = make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
   *reinterpret_cast<uint2*>(P.o + token * P.o_tok + head * P.o_head + 8 * lane) = out;
@@ -981,7 +986,7 @@ struct RegionParts {
     using K = Kind<KIND>;
     const long long a = first + kvh * all;
     const int c0 = quotient(a, share), c1 = quotient(a + (long long)(tiles - 1) * K::TILE, share);
-    if (c0 == c1) return {lead ? P.lead_o : P.own_o, lead ? P.lead_lse : P.own_lse, row, 0, 0, 1};
+    if (c0 == c1) return {lead ? P.lead_o : P.own_o, lead ? P.lead_lse : P.own_lse, row, 0, 0, 1, (long long)P.total_q * P.Hq};
     return slot_parts(*b, K::SLOT, c0, c1 - c0 + 1, row0 + gh);
   }
 };

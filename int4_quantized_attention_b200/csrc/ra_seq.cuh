@@ -427,6 +427,14 @@ __device__ __noinline__ void add_nonfinite(const SeqProb& P, VRegion g, int from
   }
 }
 
+// Whether a row's result lies in its buffer (the test build's self-check).
+__device__ __forceinline__ bool row_inside(const SeqProb& P, const ShareBuf& b, int kind, int slot, int token, int head,
+                                           int slot_row, int slot_rows) {
+  return token >= 0 && token < P.total_q && head >= 0 && head < P.Hq && (kind != OUT_FINAL || !P.shared) &&
+         (kind < OUT_LEAD || P.shared) &&
+         (kind != OUT_SLOT || (slot >= 0 && slot < 2 * b.grid && slot_row >= 0 && slot_row < slot_rows));
+}
+
 // Where a row's result goes.
 struct RowOut {
   uint8_t* h;     // final row in the output's type, or

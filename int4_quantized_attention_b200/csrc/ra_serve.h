@@ -58,6 +58,7 @@ struct SeqProb {
   ShareBuf many, few;            // the two kernels' shares
   float *lead_o, *lead_lse;      // shared > 0: [total_q * Hq](x 128), the shared region's result
   float *own_o, *own_lse;        // shared > 0: the own region's result
+  DeviceErr* err;                // for the joins' self-checks
 };
 
 // Workspace of a split call (after the 256-byte header).

@@ -248,6 +248,7 @@ bool q_map(ra::SeqMaps* m, const ra::SeqProb& P, const void* q, long long tok, l
 void bind_ws(ra::SeqProb* P, int many, int few, void* ws) {
   const ra::SeqWs L = ra::seq_ws(P->n_seqs, P->total_q, P->Hq, P->shared, many, few);
   char* b = static_cast<char*>(ws);
+  P->err = &static_cast<ra::WsHeader*>(ws)->err;
   auto floats = [&](size_t o) { return reinterpret_cast<float*>(b + o); };
   P->many.starts = reinterpret_cast<long long*>(b + L.many_starts);
   P->many.split = reinterpret_cast<ra::SplitItem*>(b + L.many_split);

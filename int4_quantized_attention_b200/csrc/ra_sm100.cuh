@@ -29,10 +29,11 @@ __device__ __forceinline__ void report(DeviceErr* e, uint32_t bit, uint32_t site
 
 // Index self-checks.  The library is also built with RA_BOUNDS_CHECK=1
 // (librotate_attn_bounds.so, a test build standing in for a memory checker):
-// there every computed global-memory index is checked against its buffer
-// before the access, and a violation records DEVERR_BOUNDS with the first
-// site and skips the access.  In the production build the checks compile
-// away.
+// there the indices that the kernels compute (rows of the outputs and of the
+// workspaces, table columns, page numbers, slots of the pool) are checked
+// against their buffers before the access, and a violation records
+// DEVERR_BOUNDS with the first site and skips the access.  In the production
+// build the checks compile away.
 #ifndef RA_BOUNDS_CHECK
 #define RA_BOUNDS_CHECK 0
 #endif
