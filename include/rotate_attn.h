@@ -373,9 +373,9 @@ ra_status ra_cache_init(const ra_cache_problem *p, const ra_cache *c, ra_stream 
 
 /* Row seqs[i] grows by n_new[i] >= 0 tokens (device int32): new pages are the
  * lowest-numbered free ones, in list order.  Their slots are unwritten.
- * The rows of a refused extend keep what they hold: writes that follow pass
- * them over, until a later extend or fork gives the row slots, a free empties
- * it, or ra_check_device_error has read the error. */
+ * The rows of a refused extend keep what they hold: writes that follow with the
+ * same workspace pass them over, until a later extend or fork gives the row
+ * slots, a free empties it, or ra_check_device_error has read the error. */
 ra_status ra_cache_extend(const ra_cache_problem *p, const ra_cache *c, const int *seqs, const int *n_new, int n,
                           void *workspace, size_t workspace_bytes, ra_stream stream);
 

@@ -458,7 +458,7 @@ __device__ int check_write(const CacheProb& c, const Ws& w, const int* seqs, con
     if (slot > (len - 1) >> c.page_shift) continue;
     const int page = c.table[(long long)row * c.max_pages + slot];
     // a page that other rows share holds their tokens too
-    if ((uint32_t)page >= (uint32_t)c.n_pages || c.refs[page] != 1) bad = BAD;
+    if ((uint32_t)page >= (uint32_t)c.n_pages || c.refs[page] > 1) bad = BAD;
   }
   if (cu_new != nullptr) {   // entries without tokens or with bad offsets have no page of their own above
     int row, count;

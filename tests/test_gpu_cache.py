@@ -434,6 +434,20 @@ def test_writes_behind_a_refused_extend(many):
     m.same()
 
 
+def test_a_state_that_counts_no_references():
+    # a program that lays out the table itself and leaves refs at 0: attention and writes need none
+    c, m = make(n_pages=9, page=16, max_seqs=2, max_pages=4)
+    c.table[0, :3] = ints([7, 2, 5])
+    c.lens[0] = 41
+    m.rows[0], m.lens[0] = [7, 2, 5], 41
+    for tokens in (1, 41):
+        k, v = rand(1, tokens, 2, D), rand(2, tokens, 2, D)
+        c.write(0, ints([0]), k, v, cu_new=ints([0, tokens]))
+        m.write(0, [0], [tokens], k, v)
+    m.same()
+    run_attention(c, m, [0], [1], 4, 0)
+
+
 def test_captured_step_on_a_full_cache():
     # extend and write in one graph: replays beyond the last page leave the cache as it was
     c, m = make(n_pages=4, page=16, max_seqs=2, max_pages=4)
