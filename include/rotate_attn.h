@@ -407,7 +407,8 @@ ra_status ra_cache_free(const ra_cache_problem *p, const ra_cache *c, const int 
 
 /* Moves pages so that the n live ones are pages 0 .. n-1: the i-th free page
  * below n takes the i-th live page at or above n, in every layer, and the
- * table follows.  Two launches. */
+ * table follows.  A row whose length is negative or more than the table holds
+ * is reported (RA_ERR_DEVICE_BOUNDS), and nothing moves.  Two launches. */
 ra_status ra_cache_compact(const ra_cache_problem *p, const ra_cache *c, void *workspace, size_t workspace_bytes,
                            ra_stream stream);
 

@@ -333,7 +333,14 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT) compact_kernel(
   const int at = ctarank() * CT + threadIdx.x;
   const Run run = page_run(c);
   const int live = (run.p1 - run.p0) - count_free(c, run);
-  const int total = cluster_scan(0, live, 0, &sh).all.pages;
+  // a row of unknown length could not follow its pages
+  int flags = 0;
+  for (int r = at; r < c.max_seqs; r += ALL)
+    if (!row_ok(c, r)) flags = BAD;
+  if (at == 0) w.jobs[0] = -1;
+  const Scan first = cluster_scan(0, live, flags, &sh);
+  if (refused(first, w.hdr, 0x5033)) return;
+  const int total = first.all.pages;
   int holes = 0, movers = 0;
   for (int p = run.p0; p < run.p1; ++p) {
     const bool is = c.refs[p] != 0;
@@ -370,7 +377,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT) compact_kernel(
 __global__ void __launch_bounds__(256) copy_kernel(CacheProb c, Ws w, int remap) {
   const int lane = threadIdx.x & 31;
   const long long warp = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5, warps = (long long)gridDim.x * 8;
-  if (remap) {
+  if (remap && w.jobs[0] >= 0) {   // -1: the compaction was refused
     for (long long row = warp; row < c.max_seqs; row += warps) {
       if (!row_ok(c, (int)row)) continue;
       const int have = pages_for(c, c.lens[row]);

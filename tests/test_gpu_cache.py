@@ -434,6 +434,23 @@ def test_writes_behind_a_refused_extend(many):
     m.same()
 
 
+@pytest.mark.parametrize("bad", [-1, 2 ** 31 - 1, 7 * 16 + 1])
+def test_compact_beside_a_row_of_unknown_length(bad):
+    # its pages would move and its table row would not follow
+    c, m = make(n_pages=20, page=16, max_seqs=4, max_pages=7)
+    c.extend(ints([0, 1, 2]), ints([50, 30, 70]))
+    m.extend([0, 1, 2], [50, 30, 70])
+    c.free(ints([0]))
+    m.free([0])
+    keep, m.lens[2] = int(c.lens[2]), bad
+    c.lens[2] = bad
+    refused(c, m, api.RA_ERR_DEVICE_BOUNDS, c.compact)
+    c.lens[2] = m.lens[2] = keep
+    c.compact()
+    m.compact()
+    m.same()
+
+
 def test_a_state_that_counts_no_references():
     # a program that lays out the table itself and leaves refs at 0: attention and writes need none
     c, m = make(n_pages=9, page=16, max_seqs=2, max_pages=4)
