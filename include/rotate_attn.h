@@ -465,7 +465,9 @@ ra_status ra_debug_int4_tile(const ra_problem *p, const ra_qkv4 *in, int bh, int
 int ra_host_chunks(const ra_problem *p, int heads_per_chunk, int *sizes, int max_chunks);
 
 /* Sets the wall-clock limit of every bounded device-side wait, in
- * microseconds (0 restores the default of 2 s); a test sets 1 and runs
+ * microseconds (0 restores the default of 2 s; the packed and paged attention
+ * adds 8 us for every 128 keys that a sequence may have, since a query tile may
+ * take that long over them); a test sets 1 and runs
  * ra_debug_timeout_probe, whose kernel waits on a barrier that nothing arms
  * and must return RA_ERR_DEVICE_TIMEOUT via ra_check_device_error. */
 void ra_debug_set_wait_timeout_us(uint32_t microseconds);

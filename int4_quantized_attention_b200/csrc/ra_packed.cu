@@ -1017,6 +1017,14 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const __grid_constant__ 
   else join_token<BF16, KIND_MANY, KIND_MANY>(P, token, h0, s, i);
 }
 
+// The list warp waits for a segment to be finished, which over millions of keys
+// takes longer than any other wait: each of the tiles it may have adds what the
+// slowest ones take (6000 cycles at 1.1 GHz), with a margin.
+uint64_t wait_limit_of(const SeqProb& p) {
+  const long long keys = p.paged ? (long long)p.max_pages << p.page_shift : p.total_k;
+  return wait_limit() + 8000ull * (uint64_t)(keys / KEYS + 1);
+}
+
 template <bool BF16>
 cudaError_t launch(const SeqProb& p, const SeqMaps& m, void* ws,
                    cudaStream_t st) {
@@ -1033,7 +1041,7 @@ cudaError_t launch(const SeqProb& p, const SeqMaps& m, void* ws,
     });
     if (e != cudaSuccess) return e;
     e = launch_after(false, kern, p.many.grid, NUM_THREADS, smem, st, p, m.q, m.k, m.v, static_cast<WsHeader*>(ws),
-                     wait_limit());
+                     wait_limit_of(p));
     if (e != cudaSuccess) return e;
   }
   if (p.few.grid > 0 && (e = launch_few_attention(p, static_cast<WsHeader*>(ws), p.many.grid > 0, st)) != cudaSuccess) return e;

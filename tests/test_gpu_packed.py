@@ -286,6 +286,24 @@ def test_a_bad_offset_anywhere_is_reported(op, n, hq):
     check(lse, wl, tl, "lse")
 
 
+def test_segments_that_outlast_a_wait(op):
+    # the tiles of one query pair take longer than the limit of a wait alone: 2500 of them some 4 ms, against 1 ms
+    tq, tk = 300 * 256, 320000
+    q, k, v = inputs(3, tq, tk, 1, 1, BF16)
+    p = api.Packed(1, 1, 1, 128, 1, 0, tq, tk, 0.0, *([128, 128] * 4))
+    assert api.packed_workspace_bytes(p) == 256          # whole items
+    api.debug_set_wait_timeout_us(1000)
+    try:
+        o, lse = op.forward(q, k, v, ints([0, tq]), ints([0, tk]), causal=False, return_lse=True)
+        op.check()
+    finally:
+        api.debug_set_wait_timeout_us(0)
+    for rows in (slice(0, 40), slice(tq - 40, tq)):
+        want, wl, tol, tl = packed(q[rows], k, v, [0, 40], [0, tk], False)
+        check(o[rows], want, tol, "o")
+        check(lse[rows], wl, tl, "lse")
+
+
 def test_no_tokens(op):
     q, k, v = inputs(2, 0, 4, 2, 2, F16)
     assert op.forward(q, k, v, ints([0, 0]), ints([0, 4])).shape == (0, 2, D)
