@@ -574,14 +574,17 @@ class PagedCache:
             _check(name, getattr(lib(), name)(self._rp, self._rc, *args, self._work.data_ptr(), self._work.numel(), stream))
 
     def extend(self, seqs, n_new) -> None:
-        """Rows `seqs` grow by `n_new` tokens (int32 device lists; -1 rows are passed over)."""
+        """Rows `seqs` grow by `n_new` tokens (int32 device lists; -1 rows are passed over).
+        Writes behind a refused extend pass its rows over until check() has
+        raised it or another call has given the row slots."""
         _ints("cache_extend", "seqs", seqs, self.device)
         _ints("cache_extend", "n_new", n_new, self.device, seqs.numel())
         self._call("ra_cache_extend", seqs.data_ptr(), n_new.data_ptr(), seqs.numel())
 
     def write(self, layer: int, seqs, k, v, cu_new=None) -> None:
         """The last tokens of rows `seqs` in one layer: k, v [tokens, Hkv, 128];
-        row i gets tokens cu_new[i] to cu_new[i + 1], or token i."""
+        row i gets tokens cu_new[i] to cu_new[i + 1], or token i.  Into pages
+        that no other row shares."""
         call = "cache_write"
         _ints(call, "seqs", seqs, self.device)
         if cu_new is not None:

@@ -18,6 +18,7 @@
 // carried out changes nothing and reports why).  Counting pages is the only
 // step over all of refs: 4 bytes per page.  The bytes themselves are moved by
 // copy_kernel over the whole GPU from a list of (source, destination, tokens).
+// A write changes no state; it too is checked as a whole before it stores.
 // A step's results depend on the lists and on prefix sums only, not on the
 // order in which threads get there.
 #include <cstdint>
@@ -558,7 +559,8 @@ __global__ void __launch_bounds__(CHECKED ? WRITE_CT : 2 * WRITE_CT)
 // with the list and with the CTAs (tokens x heads).  In every CTA / by a launch
 // of its own, 8 heads: 64 single tokens 3.2 / 6.1 us, 250 6.1 / 6.6, 64 x 8
 // tokens 5.5 / 7.1, 64 x 16 9.0 / 7.7, 250 x 3 19.7 / 7.9, one row of 1024 5.0 /
-// 7.4.  (Without any check: 2.2, 2.3, 3.7, 4.2, 4.2 and 3.4 us.)
+// 7.4, measured before pages and held rows were looked at too, which adds 0.1 to
+// 0.4 us.  (Without any check: 2.2, 2.3, 3.7, 4.2, 4.2 and 3.4 us.)
 bool short_write(const CacheProb& c, int n, int total) {
   return n <= WRITE_CT && total <= 4 * WRITE_CT && (long long)n * total * c.Hkv < 1 << 19;
 }

@@ -20,11 +20,9 @@
 //   split        all items, laid end to end, are cut into equal shares, one per
 //                CTA, whatever the lengths are; an item that crosses a border
 //                leaves partial rows (fp32) that a joining kernel puts together.
-//                For few items (below two per SM), and wherever there is a shared
-//                region.  With more, whole items win, since a share's first and
-//                last rows go through memory once more: 13 prompts of 40 to 2048
-//                tokens, 32/8 heads, 149 us against 224; one of 4096, 24 heads, both
-//                ways, 215 against 227.
+//                For few items (below two per SM), and over pages.  With more,
+//                whole items win, since a share's first and last rows go through
+//                memory once more (packed_split in ra_serve_api.cu has the figures).
 //
 // 384 threads:
 //   warps 0-3 / 4-7   softmax of tile A / B; thread t = row t = TMEM lane t
@@ -39,11 +37,13 @@
 // TMEM: S_A | S_B | O_A | O_B, 128 fp32 columns each; P overwrites the upper
 // half of S as 16-bit pairs and is the A operand of the P.V product.
 //
-// What bounds it: from some thousand tokens on the power limit (8192 and more
-// tokens run at 1.55 to 1.7 GHz and 990 W: 1040 to 1100 TFLOP/s, of 1377 that a
-// bf16 matrix product sustains there); below, what a segment costs besides its
-// tiles (a masked tile's softmax 3500 to 6000 cycles against 3340 per pair of
-// tiles in the middle of a sequence, the epilogue 4000).
+// What bounds it: from some thousand tokens on, 3340 cycles per pair of tiles,
+// whose products need 2048 and whose exponentials as many (the tensor pipe is
+// active 59 % of the time), at the 1.55 to 1.7 GHz that the power limit leaves
+// (990 W): 980 to 1100 TFLOP/s, where a bf16 matrix product sustains 1377 at that
+// limit.  Below, what a segment costs besides its tiles (a masked tile's softmax
+// 3500 to 6000 cycles, the epilogue 4000).  The softmax threads spill: a 272-byte
+// frame, 248 bytes of stores.
 //
 // Precision: S, the row statistics, O and partial rows are fp32.  P is
 // rounded to the type of V (the tensor core wants both operands alike):
@@ -54,10 +54,11 @@
 //
 // Keys past a row's limit: their scores are replaced by -inf whatever they
 // are.  Their V rows still meet a zero weight, and 0 x NaN is NaN, so in
-// every tile that some row sees in part the softmax warps clear V rows past
-// the region's end (the next sequence's rows, unwritten slots of a page) and
-// replace non-finite elements by zero, remembering the tile; the epilogue
-// then adds such elements back to the rows that do see them.
+// every tile that some row sees in part softmax warps (tile A's, where A has
+// the tile) clear V rows past the region's end (the next sequence's rows,
+// unwritten slots of a page) and replace non-finite elements by zero,
+// remembering the tile; the epilogue then adds such elements back to the rows
+// that do see them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>

@@ -140,10 +140,13 @@ ra_status check_packed(const ra_packed* p) {
   return check_out_strides(p->o_token, p->o_head, p->total_q, p->Hq);
 }
 
-// Few items leave SMs idle: split the keys instead. Below two items per SM equal shares win or tie, above it their
-// partial rows and the join cost more than the idle tail (split / whole items, causal bf16): 4 prompts of 300-400 after
-// 2000, 1.4 items per SM: 78 / 83 us; 2 of 1000-1500, 2.7 items: 72 / 57 us; 13 of 40-2048, 8 items: 168 / 153 us. A
-// single prompt of 2500 both ways, 24 heads, is the other way round (1.6 items: 104 / 95 us).
+// Few items leave SMs idle: split the keys instead. Below two items per SM equal shares mostly win or tie, above it
+// their partial rows and the join cost more than the idle tail. Time on the GPU, split / whole items, bf16 and causal
+// where nothing else is said: 2 chunks of 65-160 after 30000, 64/8 heads, 0.4 items per SM: 226 / 410 us; 4 of 300-400
+// after 2000, 32/8, 1.3 items: 75 / 81; 2 of 1000-1500, 32/8, 2.2: 58 / 47; one of 4096 both ways, 24 heads, 2.6: 191 /
+// 190; 3 of 1000-5000 both ways, 24 heads, 5.7: 374 / 364; one of 8192, 32/8, 6.9: 457 / 442; 13 of 40-2048, 32/8, 8.2:
+// 147 / 134. Two calls of few items are the other way round: one of 2500 both ways, 24 heads (1.6 items, 100 / 88), and
+// 5 texts of 1-77, 24 heads, fp16, which have one key tile each (0.8 items, 17 / 12).
 bool packed_split(const ra_packed* p) {
   return packed_items(p->total_q, p->n_seqs, 128 / (p->Hq / p->Hkv), p->Hkv) < 2 * SM_BOUND;
 }
