@@ -290,8 +290,9 @@ typedef enum { RA_FP16 = 0, RA_BF16 = 1 } ra_dtype;
  * sees no key gets zeros and a log-sum-exp of -infinity; rows behind
  * cu_q[n_seqs] are left as they were.  Keys and values that a token does not
  * see do not reach it, whatever they hold.
- * (An infinity that a token does see gives NaN instead where its weight
- * vanishes, in fp16 below 2^-31 of the row's largest: 0 times infinity.)
+ * (An infinity that a token does see with a weight that vanishes, in fp16 below
+ * 2^-31 of the row's largest, gives NaN, 0 times infinity, or the infinity, by
+ * where it lies; the same for the same call.)
  * There is no position encoding: queries and keys come encoded.  o and lse
  * overlap no input. */
 typedef struct {
